@@ -308,6 +308,127 @@ QL_API double mdbf_effective_bits(int n, int m, int r, int P, int l, int scale_b
 QL_API ql_status mdbf_select_rank(int n, int m, int P, int l, int scale_bits, double target_bits,
                            int *r_out, int *clamped);
 
+/* ------------------------------------------- rows grouped by an index ----- */
+
+/*
+ * Rows grouped by an index: the tokens of a mixture-of-experts layer by expert, the rows of a
+ * batch by the adapter of their request.  No counterpart in the pages: the grouped entry points
+ * below run the pages' products (and products beside them) for many small matrices in one call.
+ *
+ * A plan is two device arrays.  `order` lists row numbers sorted by group; `offsets` [G + 1] bounds
+ * the groups: positions i with offsets[g] <= i < offsets[g + 1] belong to group g.  group_rows and
+ * moe_route write plans; one plan serves every layer that sees the same grouping.  The kernels read
+ * offsets clamped to [0, M] (a group whose bounds decrease is empty) and skip a position whose row
+ * number is out of range, so no plan makes them read or write out of bounds.
+ */
+#define QL_MAX_GROUPS 1024
+#define QL_MAX_POSITIONS (1 << 24)   /* rows of one plan */
+
+/* The positions of a grouped product.  The struct is host memory, its pointers device memory. */
+typedef struct {
+  const int32_t *offsets; /* [G + 1] group bounds (positions) */
+  const int32_t *x_rows;  /* [M] or NULL: position i reads row x_rows[i] / x_div of x (NULL: row i) */
+  const int32_t *y_rows;  /* [M] or NULL: position i writes row y_rows[i] of y (NULL: row i); no row twice */
+  int x_div;              /* >= 1; x_rows holds slots t * k + j of a token t, with x_div = k, or rows with 1 */
+  int G, M;               /* groups (1 .. QL_MAX_GROUPS), positions (>= 0) */
+  int X, Y;               /* rows of x and of y; positions outside them are skipped */
+} ql_groups;
+
+/*
+ * group_rows -- the plan of an index: a stable counting sort.
+ *   index    device int32 [M]: the group of each row; a row outside [0, G) is in no group.
+ *   order    device int32 [M], written: the rows of group 0 ascending, then group 1, ...; the
+ *            places past offsets[G] hold -1.
+ *   offsets  device int32 [G + 1], written.
+ *   workspace device, 256-byte aligned, at least group_rows_workspace_bytes(M, G) bytes (NULL with 0
+ *            when that is 0); contents need no clearing; not shared with a concurrent call.
+ *   0 <= M <= QL_MAX_POSITIONS (QL_ERR_UNSUPPORTED above), 1 <= G <= QL_MAX_GROUPS.  The result depends on nothing but index.
+ */
+QL_API ql_status group_rows(const int32_t *index, int M, int G, int32_t *order, int32_t *offsets, void *workspace,
+                            size_t ws_bytes, ql_stream_t stream);
+QL_API size_t group_rows_workspace_bytes(int M, int G);
+
+/*
+ * moe_route -- the router of a mixture-of-experts layer and the plan of its choice.
+ *   For each token t the k experts with the largest logits, largest first, ties to the lower index
+ *   (NaN counts as larger than +inf; -0 and +0 tie).  An expert with logit -inf is never chosen: a
+ *   place that no expert fills holds expert -1 and weight 0.  weights[t][j] = p_j with
+ *   p = softmax(logits[t]) over all E, divided by the sum of the chosen p when `normalize` is set;
+ *   fp32 throughout.  A row holding NaN or +inf has NaN weights.
+ *   logits   device [T][E] of l_dtype (fp32 or bf16), contiguous.
+ *   experts  device int32 [T][k], weights device fp32 [T][k], written.
+ *   order, offsets  the plan of the T * k slots t * k + j by expert, as group_rows(experts) writes it.
+ *   workspace as group_rows, moe_route_workspace_bytes(T, E, k) bytes.
+ *   T >= 0, 1 <= E <= QL_MAX_GROUPS, 1 <= k <= min(E, 32), T * k <= QL_MAX_POSITIONS.
+ */
+QL_API ql_status moe_route(const void *logits, ql_out_dtype l_dtype, int T, int E, int k, int normalize,
+                           int32_t *experts, float *weights, int32_t *order, int32_t *offsets, void *workspace,
+                           size_t ws_bytes, ql_stream_t stream);
+QL_API size_t moe_route_workspace_bytes(int T, int E, int k);
+
+/*
+ * benq_grouped_linear -- the rows of each group through that group's own BenQ layer:
+ *     y[yr(i)][n] = sum_k lut[g][n][code(g, n, k)] * x[xr(i)][k]   for the positions i of group g,
+ *   with xr and yr from `groups`.  Rows of y that no position names keep their contents.
+ *   codes  device uint8 [G][N][3K/4], lut device bf16 bits [G][N][64], each layer as for benq_linear.
+ *   x      device bf16 bits [X][K], y device [Y][N] of y_dtype (round to nearest even of the fp32 sum).
+ *   K % 4 == 0.  K % 64 == 0 runs on the tensor cores at every size; other K on the plain cores.
+ *   The counts stay on the device: the host reads no offsets.  fp32 outputs are summed in pieces
+ *   of 512 inputs whose sums are added in fp32 (the tensor cores' own running sum truncates).
+ *   Alignment: codes, lut, x, y 16 bytes.
+ */
+QL_API ql_status benq_grouped_linear(const uint8_t *codes, const uint16_t *lut, const ql_groups *groups,
+                                     const uint16_t *x, void *y, ql_out_dtype y_dtype, int N, int K,
+                                     ql_stream_t stream);
+
+/*
+ * benq_grouped_gate_up -- h = silu(x W_g^T) * (x W_u^T) for the rows of each group with that group's
+ *   two BenQ layers (both [G][N][..] as for benq_grouped_linear); the gate is taken in fp32 as in
+ *   benq_mlp_gate_up.  Other arguments and rules as benq_grouped_linear, with h in place of y.
+ */
+QL_API ql_status benq_grouped_gate_up(const uint8_t *codes_g, const uint16_t *lut_g, const uint8_t *codes_u,
+                                      const uint16_t *lut_u, const ql_groups *groups, const uint16_t *x, void *h,
+                                      ql_out_dtype h_dtype, int N, int K, ql_stream_t stream);
+
+/*
+ * moe_combine -- the weighted sum that ends a mixture-of-experts layer:
+ *     out[t][n] = residual[t][n] + sum_j weights[t][j] * y[t k + j][n]   (j ascending, fp32)
+ *   over the places with experts[t][j] >= 0; the rows of the others are not read.
+ *   y  device [T * k][N] of y_dtype; experts int32, weights fp32 [T][k]; residual [T][N] of
+ *   out_dtype or NULL (may be out itself); out [T][N] of out_dtype.  Alignment: y, residual, out 16 bytes.
+ *   T >= 0, 1 <= k <= 32.
+ */
+QL_API ql_status moe_combine(const void *y, ql_out_dtype y_dtype, const int32_t *experts, const float *weights,
+                             const void *residual, void *out, ql_out_dtype out_dtype, int T, int k, int N,
+                             ql_stream_t stream);
+
+/*
+ * lora_add -- low-rank adapters of many requests beside a shared projection: for every layer s and
+ *   the rows i = order[p] of adapter g (offsets[g] <= p < offsets[g + 1]),
+ *     y_s[i][n] += scale[g] * sum_j B_s[g][n][j] * ( sum_k A_s[g][j][k] * x[i][k] ).
+ *   The projection (benq_linear, mdbf_linear, ...) has written y_s before; rows of no adapter keep
+ *   it.  The inner sums are fp32 and enter the second product as a bf16 pair hi + lo (2^-17
+ *   relative); an fp32 y takes one rounding of the sum, a bf16 y one rounding to nearest even.
+ *   layers   host array of S entries (1 <= S <= 4) that read the same x.
+ *   x        device bf16 bits [T][K]; order device int32 [T], offsets device int32 [G + 1]: the plan
+ *            of the rows' adapters (no row twice).
+ *   scale    device fp32 [G] or NULL (all 1).
+ *   r        the adapters' rank, 1 .. 256 (smaller ranks: zero rows of A).
+ *   workspace  device, 256-byte aligned, at least lora_workspace_bytes(S, T, r) bytes; needs no clearing;
+ *            not shared with a concurrent call.
+ *   Alignment: A, B, x, y 16 bytes.  T >= 0, K >= 1 and N >= 1 of any size.
+ */
+typedef struct {
+  const uint16_t *A;      /* bf16 [G][r][K] */
+  const uint16_t *B;      /* bf16 [G][N][r] */
+  void *y;                /* [T][N], read and written */
+  int N;                  /* output features */
+} lora_layer;
+QL_API ql_status lora_add(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order,
+                          const int32_t *offsets, const float *scale, ql_out_dtype y_dtype, int G, int T, int r,
+                          int K, void *workspace, size_t ws_bytes, ql_stream_t stream);
+QL_API size_t lora_workspace_bytes(int S, int T, int r);
+
 /* ---------------------------------------------------------------- misc ----- */
 
 /* Message for the calling thread's last non-OK status ("" if none). */

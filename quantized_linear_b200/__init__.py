@@ -36,6 +36,15 @@ class MDBFPathC(ctypes.Structure):
                 ("A_amp", _vp), ("B_amp", _vp), ("Q_U", _vp), ("Q_V", _vp)]
 
 
+class GroupsC(ctypes.Structure):
+    _fields_ = [("offsets", _vp), ("x_rows", _vp), ("y_rows", _vp), ("x_div", _i), ("G", _i), ("M", _i), ("X", _i),
+                ("Y", _i)]
+
+
+class LoraLayerC(ctypes.Structure):
+    _fields_ = [("A", _vp), ("B", _vp), ("y", _vp), ("N", _i)]
+
+
 _SIGNATURES = {
     "benq_linear": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
     "benq_linear_ws": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]),
@@ -55,6 +64,15 @@ _SIGNATURES = {
     "mdbf_noalloc_scratch_bytes": (_sz, []),
     "mdbf_effective_bits": (_d, [_i, _i, _i, _i, _i, _i]),
     "mdbf_select_rank": (_i, [_i, _i, _i, _i, _i, _d, ctypes.POINTER(_i), ctypes.POINTER(_i)]),
+    "group_rows": (_i, [_vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "group_rows_workspace_bytes": (_sz, [_i, _i]),
+    "moe_route": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_workspace_bytes": (_sz, [_i, _i, _i]),
+    "benq_grouped_linear": (_i, [_vp, _vp, ctypes.POINTER(GroupsC), _vp, _vp, _i, _i, _i, _vp]),
+    "benq_grouped_gate_up": (_i, [_vp, _vp, _vp, _vp, ctypes.POINTER(GroupsC), _vp, _vp, _i, _i, _i, _vp]),
+    "moe_combine": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "lora_add": (_i, [ctypes.POINTER(LoraLayerC), _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
+    "lora_workspace_bytes": (_sz, [_i, _i, _i]),
     "ql_last_error": (ctypes.c_char_p, []),
     "ql_check": (_i, [_vp]),
     "ql_set_pdl": (_i, [_i]),
@@ -83,7 +101,8 @@ def _c(name):
 EXPORTS = ["benq_linear", "benq_linear_ws", "benq_linear_workspace_bytes", "benq_linear_multi", "benq_mlp_gate_up",
            "benq_mlp_workspace_bytes", "benq_encode", "benq_dequant_debug", "benq_bits_per_weight", "mdbf_workspace_bytes", "mdbf_linear",
            "mdbf_linear_multi", "mdbf_linear_noalloc", "mdbf_noalloc_scratch_bytes", "mdbf_dequant_debug", "mdbf_effective_bits",
-           "mdbf_select_rank", "ql_last_error", "ql_check", "ql_set_pdl", "ql_selftest_timeout"]
+           "mdbf_select_rank", "group_rows", "group_rows_workspace_bytes", "moe_route", "moe_route_workspace_bytes", "benq_grouped_linear",
+           "benq_grouped_gate_up", "moe_combine", "lora_add", "lora_workspace_bytes", "ql_last_error", "ql_check", "ql_set_pdl", "ql_selftest_timeout"]
 
 
 class QLinearError(RuntimeError):
@@ -348,6 +367,199 @@ def mdbf_select_rank(n, m, P, l, scale_bits, target_bits):
     r, c = _i(0), _i(0)
     _check(_c("mdbf_select_rank")(n, m, P, l, scale_bits, float(target_bits), ctypes.byref(r), ctypes.byref(c)))
     return r.value, bool(c.value)
+
+
+# ------------------------------------------------------------------------------- rows grouped by an index
+
+_OUT = {torch.float32: QL_OUT_F32, torch.bfloat16: QL_OUT_BF16}
+
+
+def _arg(t, dtype, what):
+    """Address of a contiguous CUDA tensor of one dtype on the current device (decode calls run once
+    per layer and step, so the checks are kept to a few attribute reads)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _ptr(t)
+
+
+def _out(t, what):
+    d = _OUT.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return d
+
+
+def _room(workspace):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def group_rows(index, groups, order, offsets, workspace=None, stream=None):
+    """The plan of an index: order int32 [M] lists the rows of group 0, then group 1, ... (each
+    ascending, -1 past the last), offsets int32 [groups + 1] bounds them.  index int32 [M]; rows
+    with an index outside [0, groups) are in no group.  workspace: uint8 device tensor of at least
+    group_rows_workspace_bytes(M, groups) bytes when that is non-zero."""
+    M = index.numel()
+    if tuple(order.shape) != (M,) or index.dim() != 1 or tuple(offsets.shape) != (groups + 1,):
+        raise ValueError("index and order must be [M] and offsets [groups + 1]")
+    ws, nbytes = _room(workspace)
+    _check(_c("group_rows")(_arg(index, torch.int32, "index"), M, groups, _arg(order, torch.int32, "order"),
+                            _arg(offsets, torch.int32, "offsets"), ws, nbytes, _stream(stream)))
+    return order, offsets
+
+
+def group_rows_workspace_bytes(M: int, groups: int) -> int:
+    return int(_c("group_rows_workspace_bytes")(M, groups))
+
+
+def moe_route(logits, experts, weights, order, offsets, normalize=True, workspace=None, stream=None):
+    """Top-k routing and its plan: logits float32 or bf16 [T, E] -> experts int32 [T, k] (largest logit
+    first, ties to the lower index, -1 where only -inf is left), weights float32 [T, k] (softmax
+    probabilities, over the chosen when `normalize`), and the plan of the slots t * k + j by expert:
+    order int32 [T * k], offsets int32 [E + 1] (as group_rows).  workspace: uint8 device tensor of at
+    least moe_route_workspace_bytes(T, E, k) bytes when that is non-zero."""
+    T, E = logits.shape
+    k = experts.shape[1]
+    if tuple(experts.shape) != (T, k) or weights.shape != experts.shape:
+        raise ValueError("experts and weights must be [T, k]")
+    if tuple(order.shape) != (T * k,) or tuple(offsets.shape) != (E + 1,):
+        raise ValueError("order must be [T * k] and offsets [E + 1]")
+    ldt = _out(logits, "logits")
+    ws, nbytes = _room(workspace)
+    _check(_c("moe_route")(_ptr(logits), ldt, T, E, k, 1 if normalize else 0, _arg(experts, torch.int32, "experts"),
+                           _arg(weights, torch.float32, "weights"), _arg(order, torch.int32, "order"),
+                           _arg(offsets, torch.int32, "offsets"), ws, nbytes, _stream(stream)))
+    return experts, weights, order, offsets
+
+
+def moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
+    return int(_c("moe_route_workspace_bytes")(T, E, k))
+
+
+def _groups_c(G, offsets, x, y, x_rows, x_div, y_rows):
+    """ql_groups of a call: M positions come from x_rows or y_rows, or are the rows of x."""
+    if tuple(offsets.shape) != (G + 1,):
+        raise ValueError("offsets must be [G + 1]")
+    M = x.shape[0]
+    if x_rows is not None:
+        M = x_rows.numel()
+    elif x_div != 1:
+        raise ValueError("x_div needs x_rows")
+    if y_rows is not None:
+        if x_rows is not None and y_rows.numel() != M:
+            raise ValueError("x_rows and y_rows must have one entry per position")
+        M = y_rows.numel()
+    return GroupsC(_arg(offsets, torch.int32, "offsets"), None if x_rows is None else _arg(x_rows, torch.int32, "x_rows"),
+                   None if y_rows is None else _arg(y_rows, torch.int32, "y_rows"), x_div, G, M, x.shape[0], y.shape[0])
+
+
+def _grouped_layer(codes, lut, K, what):
+    G, N, B = codes.shape
+    if B * 4 != 3 * K:
+        raise ValueError(f"{what} codes must be [G, N, 3K/4]")
+    if lut.dtype not in (torch.bfloat16, torch.int16) or tuple(lut.shape) != (G, N, 64) or not lut.is_contiguous():
+        raise TypeError(f"{what} lut must be a contiguous bf16 [G, N, 64] tensor")
+
+
+def benq_grouped_linear(codes, lut, x, offsets, y, x_rows=None, x_div=1, y_rows=None, stream=None):
+    """y[yr(i)] = x[xr(i)] @ W_g^T for the positions i of every group g (offsets[g] <= i < offsets[g + 1]).
+
+    codes uint8 [G, N, 3K/4]; lut bf16 [G, N, 64]; x bf16 [X, K]; y float32 or bf16 [Y, N], whose other
+    rows keep their contents; offsets int32 [G + 1].  xr(i) = x_rows[i] // x_div, or i without x_rows;
+    yr(i) = y_rows[i] (no row twice), or i without y_rows; both int32 [M].  With moe_route's plan of k
+    slots per token: x_rows=order, x_div=k reads token rows and writes sorted rows; y_rows=order reads
+    sorted rows and writes slots."""
+    K = x.shape[1]
+    G, N = codes.shape[:2]
+    _grouped_layer(codes, lut, K, "the")
+    ydt = _out(y, "y")
+    if y.dim() != 2 or y.shape[1] != N:
+        raise ValueError("y must be [Y, N]")
+    g = _groups_c(G, offsets, x, y, x_rows, x_div, y_rows)
+    _check(_c("benq_grouped_linear")(_arg(codes, torch.uint8, "codes"), _ptr(lut), g, _arg(x, torch.bfloat16, "x"),
+                                     _ptr(y), ydt, N, K, _stream(stream)))
+    return y
+
+
+def benq_grouped_gate_up(codes_g, lut_g, codes_u, lut_u, x, offsets, h, x_rows=None, x_div=1, y_rows=None, stream=None):
+    """h[yr(i)] = silu(x[xr(i)] @ W_g^T) * (x[xr(i)] @ W_u^T) with the two layers of position i's group;
+    arguments as benq_grouped_linear, h float32 or bf16 [Y, N]."""
+    K = x.shape[1]
+    G, N = codes_g.shape[:2]
+    _grouped_layer(codes_g, lut_g, K, "gate")
+    if codes_u.shape != codes_g.shape:
+        raise ValueError("gate and up codes must have one shape")
+    _grouped_layer(codes_u, lut_u, K, "up")
+    hdt = _out(h, "h")
+    if h.dim() != 2 or h.shape[1] != N:
+        raise ValueError("h must be [Y, N]")
+    g = _groups_c(G, offsets, x, h, x_rows, x_div, y_rows)
+    _check(_c("benq_grouped_gate_up")(_arg(codes_g, torch.uint8, "gate codes"), _ptr(lut_g),
+                                      _arg(codes_u, torch.uint8, "up codes"), _ptr(lut_u), g,
+                                      _arg(x, torch.bfloat16, "x"), _ptr(h), hdt, N, K, _stream(stream)))
+    return h
+
+
+def moe_combine(y, experts, weights, out, residual=None, stream=None):
+    """out[t] = residual[t] + sum_j weights[t, j] * y[t * k + j] over the places with experts[t, j] >= 0
+    (j ascending, fp32).  y float32 or bf16 [T * k, N]; experts int32, weights float32 [T, k]; out and
+    residual (optional, may be out itself) float32 or bf16 [T, N] of one dtype."""
+    T, k = experts.shape
+    N = out.shape[1]
+    if tuple(y.shape) != (T * k, N) or weights.shape != experts.shape or out.shape[0] != T:
+        raise ValueError("y must be [T * k, N], weights [T, k] and out [T, N]")
+    ydt, odt = _out(y, "y"), _out(out, "out")
+    res = None
+    if residual is not None:
+        if residual.shape != out.shape:
+            raise ValueError("residual must be [T, N]")
+        res = _arg(residual, out.dtype, "residual")
+    _check(_c("moe_combine")(_ptr(y), ydt, _arg(experts, torch.int32, "experts"), _arg(weights, torch.float32, "weights"),
+                             res, _ptr(out), odt, T, k, N, _stream(stream)))
+    return out
+
+
+def lora_add(layers, x, order, offsets, scale=None, workspace=None, stream=None):
+    """y_s[i] += scale[g] * ((x[i] @ A_s[g]^T) @ B_s[g]^T) for the rows i of every adapter g, in place on
+    what the projection wrote; rows of no adapter keep it.
+
+    layers: 1 to 4 of (A bf16 [G, r, K], B bf16 [G, N, r], y float32 or bf16 [T, N]), all of one r and
+    one y dtype, that read the same x bf16 [T, K]; order int32 [T] and offsets int32 [G + 1]: the plan
+    of the rows' adapters (group_rows); scale float32 [G] or None; workspace: uint8 device tensor of at
+    least lora_workspace_bytes(len(layers), T, r) bytes."""
+    S = len(layers)
+    if not 1 <= S <= 4:
+        raise ValueError("lora_add takes 1 to 4 layers")
+    T, K = x.shape
+    G, r, _ = layers[0][0].shape
+    ydt = _out(layers[0][2], "y")
+    arr = (LoraLayerC * S)()
+    for A, B, y in layers:
+        N = B.shape[1]
+        if tuple(A.shape) != (G, r, K) or tuple(B.shape) != (G, N, r):
+            raise ValueError("A must be [G, r, K] and B [G, N, r], with one G and r")
+        if tuple(y.shape) != (T, N) or _out(y, "y") != ydt:
+            raise ValueError("each y must be contiguous [T, N] of the first y's dtype")
+    if tuple(order.shape) != (T,) or tuple(offsets.shape) != (G + 1,):
+        raise ValueError("order must be [T] and offsets [G + 1]")
+    if scale is not None and tuple(scale.shape) != (G,):
+        raise ValueError("scale must be [G]")
+    for i, (A, B, y) in enumerate(layers):
+        arr[i] = LoraLayerC(_arg(A, torch.bfloat16, "A"), _arg(B, torch.bfloat16, "B"), _ptr(y), B.shape[1])
+    ws, nbytes = _room(workspace)
+    _check(_c("lora_add")(arr, S, _arg(x, torch.bfloat16, "x"), _arg(order, torch.int32, "order"),
+                          _arg(offsets, torch.int32, "offsets"), None if scale is None else _arg(scale, torch.float32, "scale"),
+                          ydt, G, T, r, K, ws, nbytes, _stream(stream)))
+    return [y for _, _, y in layers]
+
+
+def lora_workspace_bytes(S: int, T: int, r: int) -> int:
+    return int(_c("lora_workspace_bytes")(S, T, r))
 
 
 def ql_check(stream=None):

@@ -1,5 +1,5 @@
 // libqlinear C ABI: argument validation, dispatch, status reporting and host-only accounting.
-// The kernels live in benq_gemv.cu, benq_gemm_sm100.cu and mdbf.cu.
+// The kernels live in the other .cu files beside it.
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -328,6 +328,140 @@ ql_status mdbf_select_rank(int n, int m, int P, int l, int scale_bits, double ta
   if (f < 1.0L) return fail(QL_ERR_INVALID_ARG, "mdbf_select_rank: target %.6f bpw is below rank 1", target_bits);
   *r_out = (int)f;
   return QL_OK;
+}
+
+static bool dtype_ok(ql_out_dtype d) { return d == QL_OUT_F32 || d == QL_OUT_BF16; }
+
+static ql_status check_workspace(const char *who, const void *ws, size_t ws_bytes, size_t need) {
+  if (ws_bytes < need || (need > 0 && !ws))
+    return fail(QL_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, ws ? ws_bytes : (size_t)0, need);
+  if (ws && !aligned(ws, 256)) return fail(QL_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", who);
+  return QL_OK;
+}
+
+size_t group_rows_workspace_bytes(int M, int G) {
+  return M < 0 || M > QL_MAX_POSITIONS || G < 1 || G > QL_MAX_GROUPS ? 0 : ql::group_rows_workspace_size(M, G);
+}
+
+ql_status group_rows(const int32_t *index, int M, int G, int32_t *order, int32_t *offsets, void *workspace,
+                     size_t ws_bytes, ql_stream_t stream) {
+  g_msg[0] = 0;
+  if (M < 0) return fail(QL_ERR_INVALID_ARG, "group_rows: M must not be negative");
+  if (M > QL_MAX_POSITIONS) return fail(QL_ERR_UNSUPPORTED, "group_rows: M = %d exceeds %d", M, QL_MAX_POSITIONS);
+  if (G < 1 || G > QL_MAX_GROUPS) return fail(QL_ERR_INVALID_ARG, "group_rows: G = %d must be in [1, %d]", G, QL_MAX_GROUPS);
+  if (!offsets || (M > 0 && (!index || !order))) return fail(QL_ERR_INVALID_ARG, "group_rows: null pointer");
+  if (!aligned(index, 4) || !aligned(order, 4) || !aligned(offsets, 4))
+    return fail(QL_ERR_ALIGNMENT, "group_rows: index, order and offsets must be 4-byte aligned");
+  const ql_status st = check_workspace("group_rows", workspace, ws_bytes, ql::group_rows_workspace_size(M, G));
+  if (st != QL_OK) return st;
+  return ql::group_rows_launch(index, M, G, order, offsets, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static bool route_sizes_ok(int T, int E, int k) {
+  return T >= 0 && E >= 1 && E <= QL_MAX_GROUPS && k >= 1 && k <= 32 && k <= E && (int64_t)T * k <= QL_MAX_POSITIONS;
+}
+
+size_t moe_route_workspace_bytes(int T, int E, int k) {
+  return route_sizes_ok(T, E, k) ? ql::moe_route_workspace_size(T, E, k) : 0;
+}
+
+ql_status moe_route(const void *logits, ql_out_dtype l_dtype, int T, int E, int k, int normalize, int32_t *experts,
+                    float *weights, int32_t *order, int32_t *offsets, void *workspace, size_t ws_bytes,
+                    ql_stream_t stream) {
+  g_msg[0] = 0;
+  if (!route_sizes_ok(T, E, k))
+    return fail(QL_ERR_INVALID_ARG, "moe_route: T = %d, E = %d, k = %d: need T >= 0, 1 <= E <= %d, 1 <= k <= min(E, 32), T k <= 2^24",
+                T, E, k, QL_MAX_GROUPS);
+  if (!dtype_ok(l_dtype)) return fail(QL_ERR_INVALID_ARG, "moe_route: bad l_dtype");
+  if (!offsets || (T > 0 && (!logits || !experts || !weights || !order)))
+    return fail(QL_ERR_INVALID_ARG, "moe_route: null pointer");
+  if (!aligned(logits, l_dtype == QL_OUT_F32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4) ||
+      !aligned(order, 4) || !aligned(offsets, 4))
+    return fail(QL_ERR_ALIGNMENT, "moe_route: pointers must be aligned to their elements");
+  const ql_status st = check_workspace("moe_route", workspace, ws_bytes, ql::moe_route_workspace_size(T, E, k));
+  if (st != QL_OK) return st;
+  return ql::moe_route_launch(logits, l_dtype, T, E, k, normalize != 0, experts, weights, order, offsets, workspace,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+static ql_status grouped(const char *who, const uint8_t *codes, const uint16_t *lut, const uint8_t *codes2,
+                         const uint16_t *lut2, bool pair, const ql_groups *g, const uint16_t *x, void *y,
+                         ql_out_dtype y_dtype, int N, int K, ql_stream_t stream) {
+  g_msg[0] = 0;
+  if (!g) return fail(QL_ERR_INVALID_ARG, "%s: null groups", who);
+  if (g->G < 1 || g->G > QL_MAX_GROUPS)
+    return fail(QL_ERR_INVALID_ARG, "%s: G = %d must be in [1, %d]", who, g->G, QL_MAX_GROUPS);
+  if (g->M < 0 || g->X < 0 || g->Y < 0 || g->x_div < 1)
+    return fail(QL_ERR_INVALID_ARG, "%s: M, X, Y must not be negative and x_div must be positive", who);
+  if (N <= 0 || K <= 0) return fail(QL_ERR_INVALID_ARG, "%s: N, K must be positive", who);
+  if (K % 4) return fail(QL_ERR_INVALID_ARG, "%s: K = %d is not a multiple of 4", who, K);
+  if ((int64_t)g->G * N >= ((int64_t)1 << 31)) return fail(QL_ERR_UNSUPPORTED, "%s: G * N must be below 2^31", who);
+  if (!dtype_ok(y_dtype)) return fail(QL_ERR_INVALID_ARG, "%s: bad output dtype", who);
+  if (!codes || !lut || (pair && (!codes2 || !lut2)) || !g->offsets) return fail(QL_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(g->offsets, 4) || !aligned(g->x_rows, 4) || !aligned(g->y_rows, 4))
+    return fail(QL_ERR_ALIGNMENT, "%s: offsets, x_rows and y_rows must be 4-byte aligned", who);
+  if (!aligned(codes, 16) || !aligned(lut, 16) || !aligned(codes2, 16) || !aligned(lut2, 16) || !aligned(x, 16) ||
+      !aligned(y, 16))
+    return fail(QL_ERR_ALIGNMENT, "%s: codes, tables, x and the output must be 16-byte aligned", who);
+  if (g->M == 0 || g->X == 0 || g->Y == 0) return QL_OK;   // no position to compute
+  if (!x || !y) return fail(QL_ERR_INVALID_ARG, "%s: null pointer", who);
+  return ql::benq_grouped_launch(codes, lut, codes2, lut2, *g, x, y, y_dtype, N, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ql_status benq_grouped_linear(const uint8_t *codes, const uint16_t *lut, const ql_groups *groups, const uint16_t *x,
+                              void *y, ql_out_dtype y_dtype, int N, int K, ql_stream_t stream) {
+  return grouped("benq_grouped_linear", codes, lut, nullptr, nullptr, false, groups, x, y, y_dtype, N, K, stream);
+}
+
+ql_status benq_grouped_gate_up(const uint8_t *codes_g, const uint16_t *lut_g, const uint8_t *codes_u,
+                               const uint16_t *lut_u, const ql_groups *groups, const uint16_t *x, void *h,
+                               ql_out_dtype h_dtype, int N, int K, ql_stream_t stream) {
+  return grouped("benq_grouped_gate_up", codes_g, lut_g, codes_u, lut_u, true, groups, x, h, h_dtype, N, K, stream);
+}
+
+ql_status moe_combine(const void *y, ql_out_dtype y_dtype, const int32_t *experts, const float *weights,
+                      const void *residual, void *out, ql_out_dtype out_dtype, int T, int k, int N, ql_stream_t stream) {
+  g_msg[0] = 0;
+  if (T < 0 || N <= 0 || k < 1 || k > 32)
+    return fail(QL_ERR_INVALID_ARG, "moe_combine: need T >= 0, N > 0 and 1 <= k <= 32");
+  if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return fail(QL_ERR_INVALID_ARG, "moe_combine: bad dtype");
+  if (!aligned(y, 16) || !aligned(residual, 16) || !aligned(out, 16) || !aligned(experts, 4) || !aligned(weights, 4))
+    return fail(QL_ERR_ALIGNMENT, "moe_combine: y, residual and out must be 16-byte aligned, experts and weights 4");
+  if (T == 0) return QL_OK;
+  if (!y || !experts || !weights || !out) return fail(QL_ERR_INVALID_ARG, "moe_combine: null pointer");
+  return ql::moe_combine_launch(y, y_dtype, experts, weights, residual, out, out_dtype, T, k, N,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t lora_workspace_bytes(int S, int T, int r) {
+  return S < 1 || S > 4 || T < 0 || r < 1 || r > 256 ? 0 : ql::lora_workspace_size(S, T, r);
+}
+
+ql_status lora_add(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order, const int32_t *offsets,
+                   const float *scale, ql_out_dtype y_dtype, int G, int T, int r, int K, void *workspace,
+                   size_t ws_bytes, ql_stream_t stream) {
+  g_msg[0] = 0;
+  if (!layers) return fail(QL_ERR_INVALID_ARG, "lora_add: null layers");
+  if (S < 1 || S > 4) return fail(QL_ERR_INVALID_ARG, "lora_add: S = %d must be in [1, 4]", S);
+  if (G < 1 || G > QL_MAX_GROUPS) return fail(QL_ERR_INVALID_ARG, "lora_add: G = %d must be in [1, %d]", G, QL_MAX_GROUPS);
+  if (T < 0 || K <= 0) return fail(QL_ERR_INVALID_ARG, "lora_add: T must not be negative and K must be positive");
+  if (r < 1 || r > 256) return fail(QL_ERR_INVALID_ARG, "lora_add: r = %d must be in [1, 256]", r);
+  if (!dtype_ok(y_dtype)) return fail(QL_ERR_INVALID_ARG, "lora_add: bad y_dtype");
+  if (!aligned(x, 16) || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(scale, 4))
+    return fail(QL_ERR_ALIGNMENT, "lora_add: x must be 16-byte aligned, order, offsets and scale 4");
+  for (int i = 0; i < S; ++i) {
+    const lora_layer &L = layers[i];
+    if (L.N <= 0) return fail(QL_ERR_INVALID_ARG, "lora_add: layer %d has N = %d", i, L.N);
+    if (!L.A || !L.B || (T > 0 && !L.y)) return fail(QL_ERR_INVALID_ARG, "lora_add: null pointer in layer %d", i);
+    if (!aligned(L.A, 16) || !aligned(L.B, 16) || !aligned(L.y, 16))
+      return fail(QL_ERR_ALIGNMENT, "lora_add: A, B and y of layer %d must be 16-byte aligned", i);
+  }
+  if (T == 0) return QL_OK;
+  if (!x || !order || !offsets) return fail(QL_ERR_INVALID_ARG, "lora_add: null pointer");
+  const ql_status st = check_workspace("lora_add", workspace, ws_bytes, ql::lora_workspace_size(S, T, r));
+  if (st != QL_OK) return st;
+  return ql::lora_add_launch(layers, S, x, order, offsets, scale, y_dtype, G, T, r, K, workspace,
+                             reinterpret_cast<cudaStream_t>(stream));
 }
 
 ql_status ql_selftest_timeout(ql_stream_t stream) {

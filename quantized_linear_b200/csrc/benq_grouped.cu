@@ -1,0 +1,93 @@
+// BenQ products grouped by an index (the experts of a mixture-of-experts layer), plain-core form:
+// y[yr(i)][n] = sum_k lut[g][n][code] x[xr(i)][k] for the positions i of group g, and the gated pair
+// h = silu(g) * u.  Any K % 4 == 0.  One warp per (group, output feature): lanes over 3-byte groups of
+// codes, the group's positions eight at a time.
+#include <algorithm>
+
+#include "ql_internal.cuh"
+
+namespace {
+
+constexpr int PB = 8;   // positions per pass over a row's codes
+
+template <bool GATED>
+__global__ void __launch_bounds__(256)
+    benq_grouped_plain_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ lut,
+                              const uint8_t *__restrict__ codes2, const uint16_t *__restrict__ lut2,
+                              const ql_groups gr, const uint16_t *__restrict__ x, void *__restrict__ y, int ydt,
+                              int N, int K) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rowbytes = 3LL * K / 4;
+  qld::pdl_trigger();
+  qld::pdl_wait();
+  const int64_t units = (int64_t)gr.G * N;
+  for (int64_t u = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; u < units;
+       u += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+    const int g = (int)(u / N), n = (int)(u - (int64_t)g * N);
+    const int p0 = max(0, min(gr.M, gr.offsets[g])), p1 = max(0, min(gr.M, gr.offsets[g + 1]));
+    for (int p = p0; p < p1; p += PB) {
+      const uint16_t *xp[PB];
+      int64_t yr[PB];
+#pragma unroll
+      for (int b = 0; b < PB; ++b) {
+        xp[b] = nullptr;
+        yr[b] = -1;
+        if (p + b < p1) {
+          const int xi = gr.x_rows ? gr.x_rows[p + b] : p + b, yi = gr.y_rows ? gr.y_rows[p + b] : p + b;
+          if (xi >= 0 && xi / gr.x_div < gr.X && (unsigned)yi < (unsigned)gr.Y) {
+            xp[b] = x + (int64_t)(gr.x_rows ? xi / gr.x_div : xi) * K;
+            yr[b] = yi;
+          }
+        }
+      }
+      float acc[GATED ? 2 : 1][PB] = {};
+#pragma unroll
+      for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+        const uint8_t *row = (m ? codes2 : codes) + u * rowbytes;
+        const uint16_t *t = (m ? lut2 : lut) + u * 64;
+        for (int q = lane; q < K / 4; q += 32) {
+          const uint32_t v = uint32_t(row[3 * q]) | (uint32_t(row[3 * q + 1]) << 8) | (uint32_t(row[3 * q + 2]) << 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint16_t w = t[(v >> (6 * e)) & 63];
+#pragma unroll
+            for (int b = 0; b < PB; ++b)
+              if (xp[b]) acc[m][b] = qld::fma_bf16(w, xp[b][4 * q + e], acc[m][b]);
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < PB; ++b) {
+        float s[2] = {acc[0][b], GATED ? acc[GATED ? 1 : 0][b] : 0.f};
+#pragma unroll
+        for (int m = 0; m < (GATED ? 2 : 1); ++m)
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) s[m] += __shfl_xor_sync(0xffffffffu, s[m], d);
+        if (lane == 0 && yr[b] >= 0) {
+          const float v = GATED ? qld::silu_mul(s[0], s[1]) : s[0];
+          if (ydt == QL_OUT_F32)
+            static_cast<float *>(y)[yr[b] * N + n] = v;
+          else
+            static_cast<uint16_t *>(y)[yr[b] * N + n] = qld::f32_to_bf16_rn(v);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+namespace ql {
+
+ql_status benq_grouped_launch(const uint8_t *codes, const uint16_t *lut, const uint8_t *codes2, const uint16_t *lut2,
+                              const ql_groups &g, const uint16_t *x, void *y, ql_out_dtype ydt, int N, int K,
+                              cudaStream_t s) {
+  const int grid = (int)std::min<int64_t>(((int64_t)g.G * N + 7) / 8, (int64_t)sm_count() * 16);
+  if (codes2)
+    launch(benq_grouped_plain_kernel<true>, grid, 256, 0, s, codes, lut, codes2, lut2, g, x, y, (int)ydt, N, K);
+  else
+    launch(benq_grouped_plain_kernel<false>, grid, 256, 0, s, codes, lut, codes2, lut2, g, x, y, (int)ydt, N, K);
+  return launch_status(codes2 ? "benq_grouped_gate_up" : "benq_grouped_linear");
+}
+
+}  // namespace ql

@@ -73,6 +73,24 @@ ql_status benq_gemm_launch(const uint8_t *codes, const uint16_t *lut, const uint
 ql_status benq_gemm_read_timeout(int *flag);
 ql_status selftest_timeout_launch(cudaStream_t s);  // reads and clears the GEMM's bounded-wait flag
 
+// rows grouped by an index (group_rows.cu, moe_combine.cu, benq_grouped.cu, lora.cu)
+size_t group_rows_workspace_size(int M, int G);
+ql_status group_rows_launch(const int32_t *index, int M, int G, int32_t *order, int32_t *offsets, void *ws,
+                            cudaStream_t s);
+size_t moe_route_workspace_size(int T, int E, int k);
+ql_status moe_route_launch(const void *logits, ql_out_dtype ldt, int T, int E, int k, bool normalize, int32_t *experts,
+                           float *weights, int32_t *order, int32_t *offsets, void *ws, cudaStream_t s);
+ql_status moe_combine_launch(const void *y, ql_out_dtype ydt, const int32_t *experts, const float *weights,
+                             const void *residual, void *out, ql_out_dtype odt, int T, int k, int N, cudaStream_t s);
+// codes2 / lut2: the up layers of the gated MLP (codes / lut are then the gate's), or null
+ql_status benq_grouped_launch(const uint8_t *codes, const uint16_t *lut, const uint8_t *codes2, const uint16_t *lut2,
+                              const ql_groups &g, const uint16_t *x, void *y, ql_out_dtype ydt, int N, int K,
+                              cudaStream_t s);
+size_t lora_workspace_size(int S, int T, int r);
+ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order,
+                          const int32_t *offsets, const float *scale, ql_out_dtype ydt, int G, int T, int r, int K,
+                          void *ws, cudaStream_t s);
+
 size_t mdbf_workspace_size(int P, int n, int m, int r, int l, int B);
 ql_status mdbf_linear_launch(const mdbf_path *paths, int P, int n, int m, int r, int l,
                              const uint16_t *x, void *y, ql_out_dtype ydt, int B, void *ws,

@@ -1,0 +1,392 @@
+"""Rows grouped by an index on the GPU: plans, the router, the experts' BenQ products and their sum.
+
+Reference: oracle/grouped.py (fp64).  Tolerances, per element:
+  * sums of K exact bf16 products in fp32, on the plain cores or on the tensor cores (which align and
+    truncate): every one of the at most K/16 + 32 roundings of a chain is below 2^-22 of the sum of
+    magnitudes s, so |y - y_ref| <= (K/16 + 32) 2^-22 s;
+  * bf16 outputs take one more rounding, at most 2^-8 of the value (half of bf16's eps);
+  * h = silu(g) u: with the bounds Eg, Eu of g and u and |silu''| <= 1/2,
+    |dh| <= |silu'(g)| Eg |u| + |silu(g)| Eu + (|silu'(g)| + 1) Eg Eu + Eg^2 |u|, plus 8 fp32 roundings of the
+    gate's own evaluation (2^-20) and fp32's smallest normal number (results below it become 0).
+"""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import benq as ob
+from oracle import grouped as og
+from tests.qlhelpers import bf16, bits16, dev
+
+pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device="cuda")
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def _ws(n):
+    return torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+
+
+def _plan(ql, index, G):
+    idx = torch.as_tensor(np.asarray(index, dtype=np.int32)).cuda()
+    M = idx.numel()
+    order, offsets = torch.full((M,), -7, **I32), torch.full((G + 1,), -7, **I32)
+    ql.group_rows(idx, G, order, offsets, workspace=_ws(ql.group_rows_workspace_bytes(M, G)))
+    return order, offsets
+
+
+# ------------------------------------------------------------------------------------------- plans
+
+@pytest.mark.parametrize("M,G", [(0, 3), (1, 1), (5, 1024), (31, 2), (32, 7), (1000, 64), (4096, 256), (4097, 256),
+                                 (20001, 1024), (300000, 5)])
+def test_group_rows(ql, M, G):
+    rng = np.random.default_rng(M + G)
+    index = rng.integers(-2, G + 2, M).astype(np.int32)      # some rows in no group
+    order, offsets = _plan(ql, index, G)
+    key = np.where((index >= 0) & (index < G), index, G)
+    want = np.argsort(key, kind="stable")
+    count = np.bincount(key, minlength=G + 1)[:G]
+    assert offsets.tolist() == np.concatenate([[0], np.cumsum(count)]).tolist()
+    n = int(count.sum())
+    assert np.array_equal(order.cpu().numpy(), np.where(np.arange(M) < n, want, -1))
+    if M <= 1000:
+        o, f = og.group_rows(index, G)
+        assert np.array_equal(order.cpu().numpy(), o) and np.array_equal(offsets.cpu().numpy(), f)
+
+
+def test_group_rows_one_group_holds_all(ql):
+    order, offsets = _plan(ql, np.full(9000, 3), 8)
+    assert torch.equal(order, torch.arange(9000, **I32)) and offsets.tolist() == [0, 0, 0, 0] + [9000] * 5
+
+
+def _route(ql, logits, k, normalize):
+    T, E = logits.shape
+    e, w = torch.full((T, k), -7, **I32), torch.full((T, k), -7.0, device="cuda")
+    order, offsets = torch.full((T * k,), -7, **I32), torch.full((E + 1,), -7, **I32)
+    ql.moe_route(logits, e, w, order, offsets, normalize=normalize, workspace=_ws(ql.moe_route_workspace_bytes(T, E, k)))
+    return e, w, order, offsets
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (3, 8, 8), (64, 33, 4), (65, 128, 8), (257, 100, 3),
+                                   (700, 256, 6), (40, 300, 32), (70, 1000, 2), (130, 1024, 1)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_moe_route(ql, T, E, k, dtype):
+    rng = np.random.default_rng(T * 7 + E)
+    l = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(dtype)
+    l[torch.from_numpy(rng.random((T, E)) < 0.1)] = -np.inf
+    l[T // 2] = -np.inf                                      # a row whose mask leaves nothing
+    l[0] = torch.round(l[0] * 2) / 2                         # many ties
+    if E > 1:
+        l[0, 0], l[0, 1] = 0.0, -0.0
+    for normalize in (True, False):
+        e, w, order, offsets = _route(ql, l.cuda(), k, normalize)
+        we, ww = og.route(l.double().numpy(), k, normalize)
+        assert np.array_equal(e.cpu().numpy(), we)
+        # exp, the sum of at most E terms and a division: (E/32 + 12) roundings of 2^-24 and the error of
+        # expf (2 ulp) and of its argument's rounding (2^-24 |l - max| <= 2^-24 * 16)
+        assert np.all(np.abs(w.cpu().numpy() - ww) <= (E / 32 + 64) * 2.0 ** -24 * ww)
+        o, f = og.group_rows(we.reshape(-1), E)
+        assert np.array_equal(order.cpu().numpy(), o) and np.array_equal(offsets.cpu().numpy(), f)
+
+
+def test_moe_route_nan_and_inf(ql):
+    l = torch.zeros(3, 40, device="cuda")
+    l[0, 7] = float("nan")
+    l[1, 5] = float("inf")
+    l[2, 9], l[2, 3] = float("inf"), -float("nan")
+    e, w, order, offsets = _route(ql, l, 2, True)
+    assert e.tolist() == [[7, 0], [5, 0], [3, 9]]
+    assert torch.isnan(w).all()
+    assert int(offsets[-1]) == 6 and sorted(order.tolist()) == list(range(6))
+
+
+# ------------------------------------------------------------------------------------------- products
+
+def _layers(G, N, K, seed):
+    ws = [synth.benq_weights(N, K, seed=seed + g) for g in range(G)]
+    return np.stack([w.codes for w in ws]), np.stack([w.lut for w in ws])
+
+
+def _sum_bound(s, K):
+    return (K / 16 + 32) * 2.0 ** -22 * s
+
+
+def _rounded(bound, ref, dtype):
+    return bound + (2.0 ** -8 * (np.abs(ref) + bound) if dtype == torch.bfloat16 else 2.0 ** -24 * np.abs(ref)) + 1e-37
+
+
+def _check_linear(ql, counts, N, K, dtype, seed, extra=0, gated=False, xdiv=2):
+    """Groups of the given sizes: gathered token rows, written to permuted rows; `extra` rows of y and positions
+    belong to no group."""
+    G, M = len(counts), sum(counts)
+    rng = np.random.default_rng(seed)
+    codes, lut = _layers(G, N, K, seed)
+    X = max(1, M // 2 + 1)
+    x = synth.activations(X, K, seed=seed + 50)
+    xr = rng.integers(0, X, M + extra).astype(np.int32)
+    yr = rng.permutation(M + extra).astype(np.int32)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    y = torch.full((M + extra, N), 77.0, dtype=dtype, device="cuda")
+    args = dict(x_rows=dev(xr * xdiv + rng.integers(0, xdiv, M + extra).astype(np.int32)), x_div=xdiv, y_rows=dev(yr))
+    ref, s = og.grouped_linear(codes, lut, x, offsets, xr[:M], K)
+    E = _sum_bound(s, K)
+    if gated:
+        c2, l2 = _layers(G, N, K, seed + 500)
+        ql.benq_grouped_gate_up(dev(codes), bits16(lut), dev(c2), bits16(l2), bf16(x), dev(offsets), y, **args)
+        u, su = og.grouped_linear(c2, l2, x, offsets, xr[:M], K)
+        Eu, g = _sum_bound(su, K), ref
+        sig = 1 / (1 + np.exp(-np.clip(g, -700, 700)))
+        d = np.abs(sig * (1 + g * (1 - sig)))
+        ref = ob.silu(g) * u
+        E = d * E * np.abs(u) + np.abs(ob.silu(g)) * Eu + (d + 1) * E * Eu + E * E * np.abs(u) + 2.0 ** -20 * np.abs(ref) + 1.2e-38
+    else:
+        ql.benq_grouped_linear(dev(codes), bits16(lut), bf16(x), dev(offsets), y, **args)
+    ql.ql_check()
+    got = y.double().cpu().numpy()
+    err = np.abs(got[yr[:M]] - ref)
+    bound = _rounded(E, ref, dtype)
+    assert np.all(err <= bound), (float((err / bound).max()), np.argwhere(err > bound)[:5].tolist())
+    assert np.all(got[yr[M:]] == 77.0)                      # rows of no group keep what they held
+
+
+CASES = [
+    # counts of the groups, N, K
+    ([1], 1, 4), ([1], 128, 64), ([0, 1, 0], 130, 64), ([3, 0, 5], 37, 100), ([2, 1], 64, 1000),
+    ([1, 0, 8, 16, 17], 256, 128), ([33, 1, 0, 64], 200, 192), ([5] * 9, 129, 320), ([200, 3], 300, 256),
+    ([193, 0, 385], 257, 576), ([1, 2], 1088, 5120), ([7, 1, 0, 20], 640, 1088), ([600], 96, 1024),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,N,K", CASES)
+def test_grouped_linear(ql, counts, N, K, dtype):
+    _check_linear(ql, counts, N, K, dtype, seed=N + K, extra=3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,N,K", CASES)
+def test_grouped_gate_up(ql, counts, N, K, dtype):
+    _check_linear(ql, counts, N, K, dtype, seed=N + K + 1, extra=2, gated=True)
+
+
+def test_grouped_linear_identity_rows_and_many_groups(ql):
+    G, N, K = 200, 40, 64
+    rng = np.random.default_rng(3)
+    counts = rng.integers(0, 4, G)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    M = int(offsets[-1])
+    codes, lut = _layers(G, N, K, 900)
+    x = synth.activations(M, K, seed=4)
+    y = torch.full((M, N), float("nan"), device="cuda")
+    ql.benq_grouped_linear(dev(codes), bits16(lut), bf16(x), dev(offsets), y)
+    ql.ql_check()
+    ref, s = og.grouped_linear(codes, lut, x, offsets, np.arange(M), K)
+    assert np.all(np.abs(y.cpu().numpy() - ref) <= _rounded(_sum_bound(s, K), ref, torch.float32))
+
+
+def test_grouped_linear_does_not_depend_on_the_batch(ql):
+    # a row's result is the same bits alone and among others of its group
+    G, N, K = 3, 200, 576
+    codes, lut = _layers(G, N, K, 40)
+    x = bf16(synth.activations(50, K, seed=41))
+    for dtype in DTYPES:
+        y = torch.zeros(50, N, dtype=dtype, device="cuda")
+        ql.benq_grouped_linear(dev(codes), bits16(lut), x, torch.tensor([0, 20, 20, 50], **I32), y)
+        one = torch.zeros(1, N, dtype=dtype, device="cuda")
+        ql.benq_grouped_linear(dev(codes), bits16(lut), x[33:34], torch.tensor([0, 0, 0, 1], **I32), one)
+        ql.ql_check()
+        assert torch.equal(one[0], y[33])
+
+
+def test_tables_of_any_order_with_nan_and_inf_in_other_groups(ql):
+    # a group's NaN table entries reach only the rows of that group
+    G, N, K = 2, 130, 128
+    codes, lut = _layers(G, N, K, 60)
+    lut = np.random.default_rng(0).permuted(lut, axis=2)
+    lut[1, :, ::2] = 0x7FC0
+    lut[1, :, 1::2] = 0x7F80
+    x = synth.activations(6, K, seed=61)
+    y = torch.zeros(6, N, device="cuda")
+    ql.benq_grouped_linear(dev(codes), bits16(lut), bf16(x), torch.tensor([0, 4, 6], **I32), y)
+    ql.ql_check()
+    ref, s = og.grouped_linear(codes[:1], lut[:1], x, [0, 4], np.arange(4), K)
+    got = y.cpu().numpy()
+    assert np.all(np.abs(got[:4] - ref) <= _rounded(_sum_bound(s, K), ref, torch.float32))
+    assert not np.isfinite(got[4:]).any()
+
+
+@pytest.mark.parametrize("K", [64, 100])
+def test_bad_plans_stay_in_bounds(ql, K):
+    # offsets beyond M or decreasing, rows out of range: those positions are skipped, the others right
+    G, N, M = 3, 70, 8
+    codes, lut = _layers(G, N, K, 70)
+    xb = synth.activations(M, K, seed=71)
+    y = torch.full((M, N), 5.0, device="cuda")
+    off = torch.tensor([-4, 4, 2, 1 << 30], **I32)            # group 0: 0..3, group 1: none, group 2: 2..7
+    off2 = torch.tensor([0, 4, 4, 8], **I32)
+    xr = torch.tensor([0, -1, 1 << 30, 3, 4, 5, 6, 7], **I32)
+    yr = torch.tensor([0, 1, 2, 3, -5, M, 1 << 30, 7], **I32)
+    c, l = dev(codes), bits16(lut)
+    ql.benq_grouped_linear(c, l, bf16(xb), off, torch.full((M, N), 5.0, device="cuda"))
+    ql.benq_grouped_gate_up(c, l, c, l, bf16(xb), off, torch.full((M, N), 5.0, device="cuda"))
+    ql.benq_grouped_linear(c, l, bf16(xb), off2, y, x_rows=xr, y_rows=yr)
+    ql.ql_check()
+    ref, s = og.grouped_linear(codes, lut, xb, [0, 4, 4, 8], np.arange(8), K)
+    got = y.cpu().numpy()
+    for i in (0, 3, 7):
+        assert np.all(np.abs(got[i] - ref[i]) <= _rounded(_sum_bound(s, K)[i], ref[i], torch.float32))
+    for i in (1, 2, 4, 5, 6):
+        assert np.all(got[i] == 5.0)
+
+
+# ------------------------------------------------------------------------------------------- combine
+
+@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (1, 8, 5120), (3, 2, 7), (65, 8, 1088), (300, 5, 513), (17, 32, 64)])
+@pytest.mark.parametrize("ydt", DTYPES)
+@pytest.mark.parametrize("odt", DTYPES)
+def test_moe_combine(ql, T, k, N, ydt, odt):
+    rng = np.random.default_rng(T + k + N)
+    y = torch.from_numpy(rng.standard_normal((T * k, N)).astype(np.float32)).to(ydt)
+    experts = rng.integers(0, 9, (T, k)).astype(np.int32)
+    experts[rng.random((T, k)) < 0.2] = -1
+    experts[T // 2] = -1                                    # a token without an expert
+    y[torch.from_numpy(experts.reshape(-1) < 0)] = float("nan")     # rows that are not read
+    w = rng.random((T, k)).astype(np.float32)
+    res = torch.from_numpy(rng.standard_normal((T, N)).astype(np.float32)).to(odt)
+    for residual in (None, res):
+        out = torch.full((T, N), float("nan"), dtype=odt, device="cuda")
+        ql.moe_combine(y.cuda(), dev(experts), dev(w), out, residual=None if residual is None else residual.cuda())
+        ref, mag = og.combine(np.nan_to_num(y.double().numpy()), experts, w, None if residual is None else residual.double().numpy())
+        bound = (k + 2) * 2.0 ** -24 * mag + (2.0 ** -8 if odt == torch.bfloat16 else 2.0 ** -24) * np.abs(ref) + 1e-37
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= bound)
+    inplace = res.cuda().clone()
+    ql.moe_combine(y.cuda(), dev(experts), dev(w), inplace, residual=inplace)
+    torch.cuda.synchronize()
+    assert torch.equal(inplace, out)
+
+
+# ------------------------------------------------------------------------------------------- together
+
+def _moe(ql, logits, x, wg, wu, wd, k, dtype=torch.bfloat16):
+    """One expert layer as a program runs it: route, gate/up, down, combine with the residual."""
+    T, E = logits.shape
+    e, w = torch.empty(T, k, **I32), torch.empty(T, k, device="cuda")
+    order, offsets = torch.empty(T * k, **I32), torch.empty(E + 1, **I32)
+    ws = _ws(ql.moe_route_workspace_bytes(T, E, k))
+    h = torch.empty(T * k, wg[0].shape[1], dtype=torch.bfloat16, device="cuda")
+    y = torch.full((T * k, wd[0].shape[1]), float("nan"), dtype=dtype, device="cuda")
+    out = torch.empty_like(x)
+
+    def go():
+        ql.moe_route(logits, e, w, order, offsets, workspace=ws)
+        ql.benq_grouped_gate_up(*wg, *wu, x, offsets, h, x_rows=order, x_div=k)
+        ql.benq_grouped_linear(*wd, h, offsets, y, y_rows=order)
+        ql.moe_combine(y, e, w, out, residual=x)
+        return out
+    return go, (e, w, order, offsets, h, y)
+
+
+def _moe_layer(E, H, F):
+    ws = [_layers(E, F, H, 2000), _layers(E, F, H, 2200), _layers(E, H, F, 2400)]
+    return ws, [(dev(c), bits16(l)) for c, l in ws]
+
+
+@pytest.mark.parametrize("T,k", [(1, 2), (3, 4), (100, 4), (700, 2)])
+def test_expert_layer(ql, T, k):
+    E, H, F = 8, 192, 128
+    host, devw = _moe_layer(E, H, F)
+    rng = np.random.default_rng(T)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[:, 5] = -np.inf                                       # an expert nobody takes
+    l[0, 1:] = -np.inf                                      # a token with one expert left
+    xb = synth.activations(T, H, seed=T)
+    x = bf16(xb)
+    go, (e, w, order, offsets, h, y) = _moe(ql, dev(l), x, *devw, k)
+    out = go()
+    ql.ql_check()
+    we, ww = og.route(l, k, True)
+    xf = ob.bf16_to_f32(xb).astype(np.float64)
+    ref, tol = xf.copy(), np.zeros_like(xf)
+    hs = h.double().cpu().numpy()
+    pos = {s: i for i, s in enumerate(order.tolist()) if s >= 0}
+    for t in range(T):
+        for j in range(k):
+            if we[t, j] < 0:
+                continue
+            hv = hs[pos[t * k + j]]
+            Wd = ob.dequant(host[2][0][we[t, j]], host[2][1][we[t, j]], F).astype(np.float64)
+            term = Wd @ hv
+            ref[t] += ww[t, j] * term
+            # y in bf16 (2^-8), its sum, the weight's roundings
+            tol[t] += ww[t, j] * (2.0 ** -8 * np.abs(term) + 1.01 * _sum_bound(np.abs(Wd) @ np.abs(hv), F)) + 2.0 ** -17 * np.abs(ww[t, j] * term)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert np.all(err <= tol + 2.0 ** -8 * (np.abs(ref) + tol) + 1e-6)
+
+
+def test_expert_layer_captured_and_replayed(ql):
+    T, k, E, H, F = 40, 4, 8, 192, 128
+    _, devw = _moe_layer(E, H, F)
+    logits = torch.randn(T, E, device="cuda")
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    go, _ = _moe(ql, logits, x, *devw, k)
+    eager = go().clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = go()
+    for seed in (1, 2):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        logits.copy_(torch.randn(T, E, device="cuda", generator=gen))
+        x.copy_(torch.randn(T, H, device="cuda", generator=gen).bfloat16())
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = out.clone()
+        assert torch.equal(replayed, go()) and not torch.equal(replayed, eager)
+    ql.ql_check()
+
+
+def test_expert_layer_on_another_stream_twice_at_once(ql):
+    T, k, E, H, F = 33, 2, 8, 192, 128
+    _, devw = _moe_layer(E, H, F)
+    logits = [torch.randn(T, E, device="cuda") for _ in range(2)]
+    xs = [torch.randn(T, H, device="cuda").bfloat16() for _ in range(2)]
+    want = [_moe(ql, l, x, *devw, k)[0]().clone() for l, x in zip(logits, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs, outs = [], []
+    for l, x, s in zip(logits, xs, streams):
+        with torch.cuda.stream(s):
+            runs.append(_moe(ql, l, x, *devw, k)[0])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for go, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                outs.append(go())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_expert_layer_chained_with_overlap_is_the_serialised_run(ql):
+    T, k, E, H, F = 24, 2, 8, 192, 128
+    _, devw = _moe_layer(E, H, F)
+    router = torch.randn(E, H, device="cuda") / H ** 0.5
+    x0 = torch.randn(T, H, device="cuda").bfloat16()
+
+    def chain(sync):
+        x = x0
+        for _ in range(4):
+            x = _moe(ql, x.float() @ router.T, x, *devw, k)[0]()
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x
+    prev = ql.ql_set_pdl(False)
+    try:
+        slow = chain(True)
+        ql.ql_set_pdl(True)
+        for _ in range(4):
+            assert torch.equal(chain(False), slow)
+    finally:
+        ql.ql_set_pdl(prev)

@@ -1,0 +1,186 @@
+"""Low-rank adapters of many requests on the GPU against oracle/grouped.py (fp64).
+
+Tolerance, per element, with s = |scale| |B| (|A| |x|): the inner sum takes at most K/8 + 64 fp32
+roundings of 2^-23 on its way (plain or tensor-core adds), the bf16 pair that enters the second product
+2^-17, the outer sum r + 8 more, so |error| <= ((K/8 + 64 + r + 8) 2^-23 + 2^-17) s; then the addition to
+y: 2^-24 of the result in fp32, 2^-8 in bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import benq as ob
+from oracle import grouped as og
+from tests.qlhelpers import bf16, bits16, dev, mdbf_dev_paths
+
+pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+def _plan(ql, index, G):
+    T = len(index)
+    order, offsets = torch.empty(T, **I32), torch.empty(G + 1, **I32)
+    n = ql.group_rows_workspace_bytes(T, G)
+    ql.group_rows(dev(np.asarray(index, dtype=np.int32)), G, order, offsets,
+                  workspace=torch.empty(n, dtype=torch.uint8, device="cuda") if n else None)
+    return order, offsets
+
+
+def _room(ql, S, T, r):
+    return torch.empty(ql.lora_workspace_bytes(S, T, r), dtype=torch.uint8, device="cuda")
+
+
+def _bits(rng, *shape, f=1.0):
+    return synth.f32_to_bf16_bits((f * rng.standard_normal(shape)).astype(np.float32))
+
+
+def _check(got, y0, A, B, xb, index, scale, K, r, dtype):
+    ref, s = og.lora(A, B, y0, xb, index, scale)
+    bound = ((K / 8 + 64 + r + 8) * 2.0 ** -23 + 2.0 ** -17) * s
+    bound = bound + (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24) * (np.abs(ref) + bound) + 1e-37
+    none = (np.asarray(index) < 0) | (np.asarray(index) >= A.shape[0])
+    bound[none] = 0                                          # rows of no adapter keep their bits
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert np.all(err <= bound), (float((err / np.maximum(bound, 1e-300)).max()), np.argwhere(err > bound)[:5].tolist())
+
+
+CASES = [
+    # T, G, r, K, Ns
+    (1, 1, 1, 1, (1,)), (1, 4, 16, 512, (256, 64, 64)), (3, 2, 5, 77, (33,)), (7, 3, 8, 256, (130, 7)),
+    (16, 16, 16, 1024, (512,)), (33, 4, 64, 640, (257, 96, 1, 40)), (64, 2, 17, 1000, (320,)), (100, 40, 4, 192, (200,)),
+    (257, 3, 32, 320, (264,)), (130, 1, 256, 512, (200,)), (600, 5, 64, 192, (136,)), (50, 3, 96, 5120, (1024,)),
+    (9, 9, 130, 264, (72,)),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("runs", [False, True])
+@pytest.mark.parametrize("T,G,r,K,Ns", CASES)
+def test_lora_add(ql, T, G, r, K, Ns, runs, dtype):
+    rng = np.random.default_rng(T * 31 + r + K)
+    index = rng.integers(-1, G + 1, T).astype(np.int32)      # -1 and G: no adapter
+    if runs:
+        index.sort()
+    xb = _bits(rng, T, K)
+    scale = (0.5 + rng.random(G)).astype(np.float32) if r % 2 == 0 else None
+    order, offsets = _plan(ql, index, G)
+    layers, host = [], []
+    for N in Ns:
+        A, B = _bits(rng, G, r, K, f=K ** -0.5), _bits(rng, G, N, r, f=r ** -0.5)
+        y = torch.from_numpy(rng.standard_normal((T, N)).astype(np.float32)).to(dtype)
+        host.append((A, B, y.double().numpy()))
+        layers.append((bf16(A), bf16(B), y.cuda()))
+    outs = ql.lora_add(layers, bf16(xb), order, offsets, scale=None if scale is None else dev(scale),
+                       workspace=_room(ql, len(Ns), T, r))
+    torch.cuda.synchronize()
+    for (A, B, y0), (_, _, y), o in zip(host, layers, outs):
+        assert o is y
+        _check(y, y0, A, B, xb, index, scale, K, r, dtype)
+
+
+def test_lora_add_without_any_adapter_in_use(ql):
+    T, G, r, K, N = 20, 3, 16, 128, 96
+    order, offsets = _plan(ql, np.full(T, -1), G)
+    y = torch.randn(T, N, device="cuda")
+    y0 = y.clone()
+    A = torch.full((G, r, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ql.lora_add([(A, torch.zeros(G, N, r, dtype=torch.bfloat16, device="cuda"), y)],
+                torch.randn(T, K, device="cuda").bfloat16(), order, offsets, workspace=_room(ql, 1, T, r))
+    torch.cuda.synchronize()
+    assert torch.equal(y, y0)
+
+
+def test_lora_add_nan_stays_in_its_rows(ql):
+    T, G, r, K, N = 40, 4, 16, 128, 96
+    rng = np.random.default_rng(5)
+    index = rng.integers(0, G, T).astype(np.int32)
+    order, offsets = _plan(ql, index, G)
+    A, B, xb = _bits(rng, G, r, K), _bits(rng, G, N, r), _bits(rng, T, K)
+    A[2] = 0x7FC0                                            # adapter 2 is NaN
+    xb[7] = 0x7F80                                           # row 7 is inf
+    y = torch.zeros(T, N, device="cuda")
+    ql.lora_add([(bf16(A), bf16(B), y)], bf16(xb), order, offsets, workspace=_room(ql, 1, T, r))
+    torch.cuda.synchronize()
+    bad = (index == 2) | (np.arange(T) == 7)
+    fin = torch.isfinite(y).all(1).cpu().numpy()
+    assert np.array_equal(fin, ~bad)
+
+
+def test_lora_add_bad_plans_stay_in_bounds(ql):
+    T, G, r, K, N = 12, 3, 8, 64, 40
+    rng = np.random.default_rng(6)
+    A, B, xb = _bits(rng, G, r, K), _bits(rng, G, N, r), _bits(rng, T, K)
+    order = torch.tensor([0, 1, -1, 1 << 30, 4, 5, T, 7, 8, 9, 10, 11], **I32)
+    y = torch.zeros(T, N, device="cuda")
+    ql.lora_add([(bf16(A), bf16(B), y)], bf16(xb), order, torch.tensor([0, 6, 6, 12], **I32), workspace=_room(ql, 1, T, r))
+    index = np.full(T, -1)
+    index[[0, 1, 4, 5]], index[[7, 8, 9, 10, 11]] = 0, 2
+    torch.cuda.synchronize()
+    _check(y, np.zeros((T, N)), A, B, xb, index, None, K, r, torch.float32)
+    for off in ([-3, 1 << 30, 4, 2], [5, 2, 7, 1 << 30]):
+        ql.lora_add([(bf16(A), bf16(B), torch.zeros(T, N, device="cuda"))], bf16(xb), torch.arange(T, **I32),
+                    torch.tensor(off, **I32), workspace=_room(ql, 1, T, r))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [1, 6, 48])
+def test_adapters_beside_both_kinds_of_projection(ql, T):
+    # q, k and v by benq_linear_multi and a down projection by mdbf_linear, each with its adapters
+    K, Ns, G, r = 1024, (1024, 256, 256), 3, 16
+    rng = np.random.default_rng(T)
+    ws = [synth.benq_weights(N, K, seed=700 + i) for i, N in enumerate(Ns)]
+    xb = synth.activations(T, K, seed=8)
+    x = bf16(xb)
+    index = rng.integers(-1, G, T).astype(np.int32)
+    order, offsets = _plan(ql, index, G)
+    ys = [torch.empty(T, N, device="cuda") for N in Ns]
+    ql.benq_linear_multi([(dev(w.codes), bits16(w.lut), y) for w, y in zip(ws, ys)], x)
+    base = [y.clone() for y in ys]
+    AB = [(_bits(rng, G, r, K, f=K ** -0.5), _bits(rng, G, N, r)) for N in Ns]
+    ql.lora_add([(bf16(a), bf16(b), y) for (a, b), y in zip(AB, ys)], x, order, offsets, workspace=_room(ql, 3, T, r))
+    n, m, rk, l, P = 256, 1024, 128, 2, 1
+    paths = synth.mdbf_paths(P, n, m, rk, l, seed=3)
+    ym = torch.empty(T, n, device="cuda")
+    ql.mdbf_linear(mdbf_dev_paths(paths), n, m, rk, l, x, ym,
+                   torch.empty(ql.mdbf_workspace_bytes(P, n, m, rk, l, T), dtype=torch.uint8, device="cuda"))
+    ym0 = ym.clone()
+    am, bm = _bits(rng, G, r, m, f=m ** -0.5), _bits(rng, G, n, r)
+    ql.lora_add([(bf16(am), bf16(bm), ym)], x, order, offsets, workspace=_room(ql, 1, T, r))
+    torch.cuda.synchronize()
+    for (a, b), y, y0 in zip(AB + [(am, bm)], ys + [ym], base + [ym0]):
+        _check(y, y0.double().cpu().numpy(), a, b, xb, index, None, K, r, torch.float32)
+    for w, y0 in zip(ws, base):
+        ref = ob.linear(w.codes, w.lut, xb, K)
+        assert np.abs(y0.cpu().numpy() - ref).max() <= 2e-3 * np.abs(ref).max()
+
+
+def test_lora_add_captured_and_replayed(ql):
+    T, G, r, K, Ns = 37, 5, 16, 256, (128, 72)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    def rnd(*s):
+        return torch.randn(*s, device="cuda", generator=gen)
+    layers = [(rnd(G, r, K).bfloat16(), rnd(G, N, r).bfloat16(), torch.zeros(T, N, device="cuda")) for N in Ns]
+    index = torch.randint(-1, G, (T,), generator=gen, **I32)
+    x, order, offsets, ws = rnd(T, K).bfloat16(), torch.empty(T, **I32), torch.empty(G + 1, **I32), _room(ql, 2, T, r)
+
+    def go():
+        for _, _, y in layers:
+            y.zero_()
+        ql.group_rows(index, G, order, offsets)
+        return ql.lora_add(layers, x, order, offsets, workspace=ws)
+    go()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go()
+    for _ in range(3):
+        index.copy_(torch.randint(-1, G, (T,), generator=gen, **I32))
+        x.copy_(rnd(T, K).bfloat16())
+        g.replay()
+        torch.cuda.synchronize()
+        got = [y.clone() for _, _, y in layers]
+        go()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, y) for a, (_, _, y) in zip(got, layers))

@@ -1,0 +1,158 @@
+"""Refusals of the grouped entry points and of their binding (CPU only: no call launches a kernel)."""
+import ctypes
+
+import pytest
+import torch
+
+A = 1 << 20    # never dereferenced: every call below fails validation, or has nothing to do
+
+
+def _groups(ql, **kw):
+    f = dict(offsets=A, x_rows=None, y_rows=None, x_div=1, G=4, M=8, X=8, Y=8)
+    f.update(kw)
+    return ql.GroupsC(*[f[n] for n, _ in ql.GroupsC._fields_])
+
+
+def test_group_rows_refusals(ql):
+    f = ql.lib().group_rows
+    assert f(A, -1, 4, A, A, None, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 8, 0, A, A, None, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 8, 1025, A, A, None, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, (1 << 24) + 1, 4, A, A, A, 1 << 30, None) == ql.QL_ERR_UNSUPPORTED
+    assert f(None, 8, 4, A, A, None, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 8, 4, A, None, None, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A + 2, 8, 4, A, A, None, 0, None) == ql.QL_ERR_ALIGNMENT
+    need = ql.group_rows_workspace_bytes(100000, 64)
+    assert need > 0 and need % 256 == 0 and ql.group_rows_workspace_bytes(100, 64) == 0
+    assert f(A, 100000, 64, A, A, None, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 100000, 64, A, A, A, need - 1, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 100000, 64, A, A, A + 16, need, None) == ql.QL_ERR_ALIGNMENT
+
+
+def test_moe_route_refusals(ql):
+    f = ql.lib().moe_route
+    ok = [A, 0, 8, 16, 4, 1, A, A, A, A, None, 0, None]
+
+    def call(**kw):
+        a = list(ok)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return f(*a)
+    assert call(_2=-1) == ql.QL_ERR_INVALID_ARG                  # T
+    assert call(_3=1025) == ql.QL_ERR_INVALID_ARG                # E
+    assert call(_4=0) == ql.QL_ERR_INVALID_ARG                   # k
+    assert call(_4=17) == ql.QL_ERR_INVALID_ARG                  # k > E
+    assert call(_3=64, _4=33) == ql.QL_ERR_INVALID_ARG           # k > 32
+    assert call(_2=1 << 22, _4=8) == ql.QL_ERR_INVALID_ARG       # T * k
+    assert call(_1=3) == ql.QL_ERR_INVALID_ARG                   # dtype
+    assert call(_0=None) == ql.QL_ERR_INVALID_ARG
+    assert call(_9=None) == ql.QL_ERR_INVALID_ARG
+    assert call(_0=A + 2) == ql.QL_ERR_ALIGNMENT
+    need = ql.moe_route_workspace_bytes(1000, 16, 4)
+    assert need > 0 and ql.moe_route_workspace_bytes(64, 16, 4) == 0
+    assert call(_2=1000) == ql.QL_ERR_INVALID_ARG                # no workspace
+    assert call(_2=1000, _10=A, _11=need - 1) == ql.QL_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_refusals(ql, gated):
+    lib = ql.lib()
+
+    def call(g, N=8, K=64, dt=0, codes=A, x=A, y=A):
+        if gated:
+            return lib.benq_grouped_gate_up(codes, A, A, A, g, x, y, dt, N, K, None)
+        return lib.benq_grouped_linear(codes, A, g, x, y, dt, N, K, None)
+    assert call(None) == ql.QL_ERR_INVALID_ARG
+    for bad in (dict(G=0), dict(G=1025), dict(M=-1), dict(X=-1), dict(Y=-1), dict(x_div=0), dict(offsets=None)):
+        assert call(_groups(ql, **bad)) == ql.QL_ERR_INVALID_ARG, bad
+    assert call(_groups(ql), N=0) == ql.QL_ERR_INVALID_ARG
+    assert call(_groups(ql), K=66) == ql.QL_ERR_INVALID_ARG
+    assert call(_groups(ql), dt=2) == ql.QL_ERR_INVALID_ARG
+    assert call(_groups(ql), codes=None) == ql.QL_ERR_INVALID_ARG
+    assert call(_groups(ql), codes=A + 8) == ql.QL_ERR_ALIGNMENT
+    assert call(_groups(ql), x=None) == ql.QL_ERR_INVALID_ARG
+    assert call(_groups(ql), y=A + 4) == ql.QL_ERR_ALIGNMENT
+    assert call(_groups(ql, x_rows=A + 2)) == ql.QL_ERR_ALIGNMENT
+    assert call(_groups(ql, G=1024), N=1 << 22) == ql.QL_ERR_UNSUPPORTED
+    assert call(_groups(ql, M=0), x=None, y=None) == ql.QL_OK    # no positions: nothing to do
+
+
+def test_combine_refusals(ql):
+    f = ql.lib().moe_combine
+    assert f(A, 0, A, A, None, A, 0, -1, 2, 8, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 0, A, A, None, A, 0, 4, 33, 8, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 0, A, A, None, A, 0, 4, 2, 0, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 0, A, A, None, A, 5, 4, 2, 8, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A, 0, A, None, None, A, 0, 4, 2, 8, None) == ql.QL_ERR_INVALID_ARG
+    assert f(A + 8, 0, A, A, None, A, 0, 4, 2, 8, None) == ql.QL_ERR_ALIGNMENT
+    assert f(A, 0, A, A, A + 4, A, 0, 4, 2, 8, None) == ql.QL_ERR_ALIGNMENT
+    assert f(None, 0, None, None, None, None, 0, 0, 2, 8, None) == ql.QL_OK
+
+
+def test_lora_refusals(ql):
+    f = ql.lib().lora_add
+    arr = (ql.LoraLayerC * 5)(*[ql.LoraLayerC(A, A, A, 8) for _ in range(5)])
+    need = ql.lora_workspace_bytes(1, 4, 16)
+    assert need >= 4 * 16 * 4 and ql.lora_workspace_bytes(5, 4, 16) == 0
+
+    def call(layers=arr, S=1, x=A, order=A, offsets=A, scale=None, dt=0, G=2, T=4, r=16, K=64, ws=A, nbytes=need):
+        return f(layers, S, x, order, offsets, scale, dt, G, T, r, K, ws, nbytes, None)
+    assert call(layers=None) == ql.QL_ERR_INVALID_ARG
+    for bad in (dict(S=0), dict(S=5), dict(G=0), dict(G=1025), dict(T=-1), dict(r=0), dict(r=257), dict(K=0), dict(dt=9),
+                dict(x=None), dict(order=None), dict(offsets=None), dict(ws=None, nbytes=0), dict(nbytes=need - 1)):
+        assert call(**bad) == ql.QL_ERR_INVALID_ARG, bad
+    for bad in (dict(x=A + 2), dict(order=A + 2), dict(scale=A + 1), dict(ws=A + 32)):
+        assert call(**bad) == ql.QL_ERR_ALIGNMENT, bad
+    arr[0] = ql.LoraLayerC(A, A + 8, A, 8)
+    assert call() == ql.QL_ERR_ALIGNMENT
+    arr[0] = ql.LoraLayerC(A, A, A, 0)
+    assert call() == ql.QL_ERR_INVALID_ARG
+    arr[0] = ql.LoraLayerC(A, None, A, 8)
+    assert call() == ql.QL_ERR_INVALID_ARG
+    arr[0] = ql.LoraLayerC(A, A, A, 8)
+    assert call(T=0, x=None, order=None, offsets=None) == ql.QL_OK
+
+
+def test_binding_refuses_wrong_tensors(ql):
+    i32, bf, f32 = torch.int32, torch.bfloat16, torch.float32
+    G, N, K, M = 2, 4, 64, 3
+    codes, lut = torch.zeros(G, N, 3 * K // 4, dtype=torch.uint8), torch.zeros(G, N, 64, dtype=bf)
+    x, y, off = torch.zeros(M, K, dtype=bf), torch.zeros(M, N), torch.zeros(G + 1, dtype=i32)
+    rows = torch.zeros(M, dtype=i32)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        ql.benq_grouped_linear(codes, lut, x, off, y)
+    with pytest.raises(ValueError, match="codes must be"):
+        ql.benq_grouped_linear(codes[..., :-4], lut, x, off, y)
+    with pytest.raises(TypeError, match="lut"):
+        ql.benq_grouped_linear(codes, lut.float(), x, off, y)
+    with pytest.raises(TypeError, match="y must be"):
+        ql.benq_grouped_linear(codes, lut, x, off, y.half())
+    with pytest.raises(ValueError, match="contiguous"):
+        ql.benq_grouped_linear(codes, lut, x, off, torch.zeros(N, M).T)
+    with pytest.raises(ValueError, match="one shape"):
+        ql.benq_grouped_gate_up(codes, lut, codes[:1], lut, x, off, y)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        ql.group_rows(rows, G, rows.clone(), off)
+    with pytest.raises(ValueError, match="offsets"):
+        ql.group_rows(rows, G, rows.clone(), off[:-1])
+    with pytest.raises(ValueError, match="order must be"):
+        ql.moe_route(torch.zeros(M, 8), torch.zeros(M, 2, dtype=i32), torch.zeros(M, 2), rows, torch.zeros(9, dtype=i32))
+    with pytest.raises(ValueError, match="y must be"):
+        ql.moe_combine(y, torch.zeros(M, 2, dtype=i32), torch.zeros(M, 2), torch.zeros(M, N))
+    with pytest.raises(TypeError, match="residual"):
+        ql.moe_combine(torch.zeros(2 * M, N), torch.zeros(M, 2, dtype=i32), torch.zeros(M, 2), torch.zeros(M, N),
+                       residual=torch.zeros(M, N, dtype=bf))
+    a, b = torch.zeros(G, 4, K, dtype=bf), torch.zeros(G, N, 4, dtype=bf)
+    with pytest.raises(ValueError, match="1 to 4 layers"):
+        ql.lora_add([], x, rows, off)
+    with pytest.raises(ValueError, match="A must be"):
+        ql.lora_add([(a, b[:1], y)], x, rows, off)
+    with pytest.raises(ValueError, match="each y"):
+        ql.lora_add([(a, b, y), (a, b, y.to(bf))], x, rows, off)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        ql.lora_add([(a, b, y)], x, rows, off)
+    with pytest.raises(ValueError, match="x_div"):
+        ql._groups_c(G, off, x, y, None, 2, None)
+    with pytest.raises(ValueError, match="one entry"):
+        ql._groups_c(G, off, x, y, rows, 1, rows[:2])
+    assert f32 is torch.float32 and ctypes.sizeof(ql.GroupsC) == 48

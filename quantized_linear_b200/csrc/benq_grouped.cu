@@ -1,4 +1,5 @@
-// BenQ products grouped by an index (the experts of a mixture-of-experts layer), plain-core form:
+// BenQ products grouped by an index (the experts of a mixture-of-experts layer), plain-core form for the K that
+// the tensor-core kernel does not take (benq_grouped_sm100.cu, K % 64 == 0):
 // y[yr(i)][n] = sum_k lut[g][n][code] x[xr(i)][k] for the positions i of group g, and the gated pair
 // h = silu(g) * u.  Any K % 4 == 0.  One warp per (group, output feature): lanes over 3-byte groups of
 // codes, the group's positions eight at a time.
@@ -14,7 +15,7 @@ template <bool GATED>
 __global__ void __launch_bounds__(256)
     benq_grouped_plain_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ lut,
                               const uint8_t *__restrict__ codes2, const uint16_t *__restrict__ lut2,
-                              const ql_groups gr, const uint16_t *__restrict__ x, void *__restrict__ y, int ydt,
+                              const ql_groups gr, const uint16_t *x, void *y, int ydt,
                               int N, int K) {
   const int lane = threadIdx.x & 31;
   const int64_t rowbytes = 3LL * K / 4;
@@ -82,6 +83,8 @@ namespace ql {
 ql_status benq_grouped_launch(const uint8_t *codes, const uint16_t *lut, const uint8_t *codes2, const uint16_t *lut2,
                               const ql_groups &g, const uint16_t *x, void *y, ql_out_dtype ydt, int N, int K,
                               cudaStream_t s) {
+  // whole 64-code blocks (and so 16-byte aligned code rows) run on the tensor cores at every size
+  if (K % 64 == 0) return benq_grouped_mma_launch(codes, lut, codes2, lut2, g, x, y, ydt, N, K, s);
   const int grid = (int)std::min<int64_t>(((int64_t)g.G * N + 7) / 8, (int64_t)sm_count() * 16);
   if (codes2)
     launch(benq_grouped_plain_kernel<true>, grid, 256, 0, s, codes, lut, codes2, lut2, g, x, y, (int)ydt, N, K);

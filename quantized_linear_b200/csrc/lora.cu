@@ -26,9 +26,9 @@ __device__ __forceinline__ int group_at(const int32_t *offsets, int G, int p, in
 }
 
 __global__ void __launch_bounds__(256)
-    lora_shrink_plain_kernel(const Layers L, int S, const uint16_t *__restrict__ x, const int32_t *__restrict__ order,
-                             const int32_t *__restrict__ offsets, const float *__restrict__ scale, int G, int T, int r,
-                             int K, float *__restrict__ t) {
+    lora_shrink_plain_kernel(const Layers L, int S, const uint16_t *x, const int32_t *order,
+                             const int32_t *offsets, const float *scale, int G, int T, int r,
+                             int K, float *t) {
   const int lane = threadIdx.x & 31;
   qld::pdl_trigger();
   qld::pdl_wait();
@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    lora_expand_plain_kernel(const Layers L, int S, const int32_t *__restrict__ order, const int32_t *__restrict__ offsets,
-                             int ydt, int G, int T, int r, const float *__restrict__ t) {
+    lora_expand_plain_kernel(const Layers L, int S, const int32_t *order, const int32_t *offsets,
+                             int ydt, int G, int T, int r, const float *t) {
   qld::pdl_trigger();
   qld::pdl_wait();
   for (int s = 0; s < S; ++s) {

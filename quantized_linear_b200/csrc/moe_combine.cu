@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(256)
       float acc[COLS] = {};
 #pragma unroll 4
       for (int j = 0; j < k; ++j) {
-        if (__ldg(experts + t * k + j) < 0) continue;
-        const float w = __ldg(weights + t * k + j);
+        if (__ldcg(experts + t * k + j) < 0) continue;
+        const float w = __ldcg(weights + t * k + j);
         float v[COLS];
         load8<YF32>(y, (size_t)(t * k + j) * N + n, v);
 #pragma unroll
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(256)
     } else {
       float acc = 0.f;
       for (int j = 0; j < k; ++j)
-        if (__ldg(experts + t * k + j) >= 0)
-          acc = fmaf(__ldg(weights + t * k + j), load1(y, (size_t)(t * k + j) * N + n, YF32), acc);
+        if (__ldcg(experts + t * k + j) >= 0)
+          acc = fmaf(__ldcg(weights + t * k + j), load1(y, (size_t)(t * k + j) * N + n, YF32), acc);
       const size_t o = (size_t)t * N + n;
       if (residual) acc += load1(residual, o, OF32);
       if (OF32)

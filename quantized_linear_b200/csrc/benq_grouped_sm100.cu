@@ -15,10 +15,13 @@
 // Per 64-wide K block and SM that is 256 + 48 wavefronts of lookups and codes, 48 of code writes and
 // n/2 + n/2 of X for n positions, against 2 n clocks of MMA.
 //
-// Roles (512 threads per CTA): warp 0 loads X (rows gathered by x_rows, or tiles); warp 1 issues the MMAs
-// (even CTA) or relays decoded blocks (odd CTA); warp 2 loads codes and tables; warps 4-7 drain the
-// accumulators; warps 8-15, two warpgroups on alternate K blocks, decode.  Accumulators are two slots of
-// 192 columns, so one tile's epilogue overlaps the next tile's MMAs.
+// Roles (640 threads per CTA): warps 0 and 3 load X on alternate steps (rows gathered by x_rows: a gather of four rows
+// takes about 40 clocks to issue, or tiles); warp 1 issues the MMAs (even CTA); warp 2 loads codes and, between them,
+// lays out the next tile's tables; warps 4-7 and 8-11 drain the accumulator slots 0 and 1; warps 12-19, two
+// warpgroups, decode the two K blocks of a step.  Accumulators are two
+// slots of 192 columns, so one tile's epilogue overlaps the next tile's MMAs.  The decoders of the odd CTA arrive at
+// the even CTA's barrier with relaxed semantics: what they hand over is in tensor memory, which the tcgen05 fences
+// order (a cluster-scope release by one relaying thread took 1300 clocks per K block and set the kernel's pace).
 //
 // The gated form gives each warp of lanes 16 gate rows and the same features' 16 up rows: silu(g) * u then needs
 // one exchange between the halves of a warp.
@@ -42,53 +45,58 @@ using namespace pairgemm;
 
 constexpr int RW = 128;                        // rows of W per CTA and tile
 constexpr int NS = 192;                        // positions per accumulator slot (the MMA's N)
-constexpr int NT = 2 * NS;                     // positions per tile
-constexpr int XR = NT / 2;                     // positions whose x rows one CTA loads
-constexpr int SX = 4, SA = 4, SC = 3;          // stages: x, decoded W, codes
-constexpr int X_BYTES = XR * 128;              // 24 KB: 64 bf16 per row
+constexpr int NT = 2 * NS;                     // positions per tile at most
+constexpr int SA = 2, SC = 3;                  // stages: decoded W (steps), codes
+constexpr int X_RING = 96 * 1024;              // x stages of one step each: two 64-column blocks of half a tile's rows
+constexpr int SX_MAX = 8;
 constexpr int X_BOX = 32;                      // rows per copy when rows are not gathered
-constexpr int CKB = 3;                         // K blocks per code stage: rows of 144 bytes, a 16-byte load of 8
-constexpr int C_ROW = CKB * 48;                // rows is free of bank conflicts
+constexpr int CKB = 3;                         // K blocks per code stage: rows of 144 bytes, so that a 16-byte load
+constexpr int C_ROW = CKB * 48;                // of 8 rows at a time is free of bank conflicts
 constexpr int C_BYTES = RW * C_ROW;            // 18 KB
-constexpr int LUT_BYTES = RW * 128;            // 16 KB
-constexpr int TBL_BYTES = 4 * 8192;            // lane-private tables: 4 warps of rows x [64][32] words
+constexpr int TBL_BYTES = 4 * 8192;            // lane-private tables: 4 warps of rows x [64][32] words, two buffers
 constexpr int NDW = 8;                         // decoder warps (two warpgroups)
-constexpr int THREADS = 512;
-constexpr int D_COL = 0, A_COL = NT;           // tensor memory columns: accumulators, then SA stages of 32
+constexpr int THREADS = 640;
+constexpr int D_COL = 0, A_COL = NT;           // tensor memory columns: accumulators, then SA steps of 2 x 32
 constexpr int MAX_SEG = NT / 16;               // runs of K blocks with an accumulator each (fp32 outputs)
-constexpr int SEG_KB = 8;
-constexpr int OFF_X = TBL_BYTES;
-constexpr int OFF_C = OFF_X + SX * X_BYTES;
-constexpr int OFF_LUT = OFF_C + SC * C_BYTES;
-constexpr int OFF_BAR = OFF_LUT + LUT_BYTES;
-constexpr int NBAR = 2 * SX + 3 * SA + 2 * SC + 2 + 4 + 8;
-constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor-memory address, abort flag
+constexpr int SEG_STEPS = 4;                   // 512 inputs
+// Shared memory: barriers and the tile counts in front of the tables, which start on 8 KB (a lookup ORs the code into
+// the address).  The front's size puts them there when dynamic shared memory starts at 1 KB, as it does after the
+// kilobyte that the system keeps; the kernel checks it.
+constexpr int FRONT = 8192 - 1024;
+constexpr int NBAR = 2 * SX_MAX + 2 * SA + 2 * SC + 8;
+constexpr int OFF_MISC = NBAR * 8;             // tensor-memory address, abort flag
 constexpr int OFF_GRP = OFF_MISC + 16;         // token tiles before each group, int [G + 1]
-static_assert(A_COL + 32 * SA <= 512, "tensor memory");
-static_assert(OFF_X % 1024 == 0 && X_BYTES % 1024 == 0 && (XR / 2) * 128 % 1024 == 0, "swizzle atoms");
-static_assert(OFF_C % 128 == 0 && C_BYTES % 128 == 0 && OFF_LUT % 128 == 0 && OFF_BAR % 8 == 0, "alignment");
-constexpr size_t smem_bytes(int G) { return OFF_GRP + (size_t)(G + 1) * sizeof(int) + 8192; }
-static_assert(smem_bytes(QL_MAX_GROUPS) <= 232448, "shared memory");
+constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
+constexpr int OFF_C = OFF_X + X_RING;
+constexpr int STG_BYTES = 512;                 // per epilogue warp: 8 positions x 32 features of bf16, or 16 x 16
+constexpr int OFF_STG = OFF_C + SC * C_BYTES;
+constexpr int SMEM_BYTES = FRONT + OFF_STG + 8 * STG_BYTES;
+static_assert(OFF_GRP + (QL_MAX_GROUPS + 1) * 4 <= FRONT, "front");
+static_assert(A_COL + 64 * SA <= 512, "tensor memory");
+static_assert(OFF_X % 1024 == 0 && OFF_C % 128 == 0 && C_BYTES % 128 == 0 && OFF_STG % 128 == 0, "alignment");
+static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr uint16_t PAIR = 0x3;
 
 __device__ int g_grouped_timeout = 0;
 
 struct Bars {
-  uint32_t full_x, empty_x, dec_done, peer_a, empty_a, full_c, empty_c, lut_full, lut_empty, tbl_free, tbl_ready,
-      acc_full, acc_empty;
+  // full_x, ready_a: a step's x rows (of both CTAs) and decoded W (of both CTAs' decoders) are there, in the even
+  // CTA; empty_x, empty_a: its MMAs are done, in both.
+  uint32_t full_x, empty_x, ready_a, empty_a, full_c, empty_c, tbl_full, tbl_empty, acc_full, acc_empty;
   __device__ Bars(uint32_t b)
-      : full_x(b), empty_x(full_x + 8 * SX), dec_done(empty_x + 8 * SX), peer_a(dec_done + 8 * SA),
-        empty_a(peer_a + 8 * SA), full_c(empty_a + 8 * SA), empty_c(full_c + 8 * SC), lut_full(empty_c + 8 * SC),
-        lut_empty(lut_full + 8), tbl_free(lut_empty + 8), tbl_ready(tbl_free + 8 * 4), acc_full(tbl_ready + 8 * 4),
-        acc_empty(acc_full + 8 * 2) {}
+      : full_x(b), empty_x(full_x + 8 * SX_MAX), ready_a(empty_x + 8 * SX_MAX), empty_a(ready_a + 8 * SA),
+        full_c(empty_a + 8 * SA), empty_c(full_c + 8 * SC), tbl_full(empty_c + 8 * SC), tbl_empty(tbl_full + 8 * 2),
+        acc_full(tbl_empty + 8 * 2), acc_empty(acc_full + 8 * 2) {}
 };
-static_assert(NBAR >= 2 * SX + 3 * SA + 2 * SC + 2 + 8 + 4, "barriers");
 
 struct Args {
   const uint16_t *lut, *lut2;
   ql_groups g;
   void *y;
-  int ydt, N, K, ntl, nt_max, seg, nseg;   // tiles of W rows per group, positions per tile, K blocks per run, runs
+  int ydt, N, K, ntl, nt_max;   // tiles of W rows per group, positions per tile at most
+  int xr, xst;                       // rows per 64-column block of an x stage, x stages
+  int vec;                           // bf16 rows of whole 16-byte pieces
+  int seg, nseg;                     // steps per run of its own accumulator, runs
 };
 
 // One tile: W rows of index wt, positions [p0, p1) of group g; nh columns per MMA, one MMA per half.
@@ -97,17 +105,17 @@ struct Tile {
 };
 
 // Which accumulator slots a tile takes (the same sequence in the MMA issuer and the epilogue): a tile of one slot
-// takes the other than the last, a tile of two takes both.  used[s] counts a slot's tiles for its barriers' phases.
+// takes the other than the last, a tile of two takes both.  used0 and used1 count the slots' tiles for their barriers' phases.
 struct Slots {
-  int next = 0, used[2] = {0, 0};
+  int next = 0, used0 = 0, used1 = 0;
   __device__ __forceinline__ int take(int slots) {
     const int s = slots == 2 ? 0 : next;
     next = slots == 2 ? 0 : next ^ 1;
     return s;
   }
   __device__ __forceinline__ void done(int first, int slots) {
-    used[0] += (slots == 2 || first == 0);
-    used[1] += (slots == 2 || first == 1);
+    used0 += (slots == 2 || first == 0);
+    used1 += (slots == 2 || first == 1);
   }
 };
 
@@ -154,18 +162,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         const __grid_constant__ CUtensorMap map_c2, const Args a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
-  const uint32_t sbase = (raw + 8191u) & ~8191u;   // the lookups OR the code into the table's address
-  unsigned char *const sm = smem_raw + (sbase - raw);
-  const Bars bar(sbase + OFF_BAR);
-  const uint32_t tmem_slot = sbase + OFF_MISC;
-  int *const cum = reinterpret_cast<int *>(sm + OFF_GRP);   // token tiles before each group
+  const uint32_t sbase = (raw + FRONT + 8191u) & ~8191u;
+  uint32_t have;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(have));
+  if (sbase + (SMEM_BYTES - FRONT) - raw > have) {   // the same in every CTA: none goes on
+    if (threadIdx.x == 0) atomicExch(&g_grouped_timeout, 2);
+    return;
+  }
+  const Bars bar(raw);
+  const uint32_t tmem_slot = raw + OFF_MISC;
+  int *const cum = reinterpret_cast<int *>(smem_raw + OFF_GRP);   // token tiles before each group
   const int G = a.g.G;
   const uint32_t rank = sm100::cluster_ctarank();
   const bool lead = rank == 0;
   const Waiter wt{tmem_slot + 4, sm100::mapa_shared(tmem_slot + 4, rank ^ 1u)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int nkb = a.K / 64;
+  const int nkb = a.K / 64, nst = (nkb + 1) / 2;   // K blocks, steps
+  const uint32_t xblk = a.xr * 128;                // bytes of a 64-column block of an x stage
   bool ok = true;
   // a wait of a whole warp: no lane goes on alone when one gave up
   auto warp_wait = [&](uint32_t b, uint32_t parity, bool cluster_scope) {
@@ -173,26 +187,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < SX; ++s) {
+    for (int s = 0; s < SX_MAX; ++s) {
       sm100::mbar_init(bar.full_x + 8 * s, 1);
       sm100::mbar_init(bar.empty_x + 8 * s, 1);
     }
     for (int s = 0; s < SA; ++s) {
-      sm100::mbar_init(bar.dec_done + 8 * s, 4);
-      sm100::mbar_init(bar.peer_a + 8 * s, 1);
+      sm100::mbar_init(bar.ready_a + 8 * s, 2 * NDW);   // the decoder warps of both CTAs
       sm100::mbar_init(bar.empty_a + 8 * s, 1);
     }
     for (int s = 0; s < SC; ++s) {
       sm100::mbar_init(bar.full_c + 8 * s, 1);
       sm100::mbar_init(bar.empty_c + 8 * s, NDW);
     }
-    sm100::mbar_init(bar.lut_full, 1);
-    sm100::mbar_init(bar.lut_empty, NDW);
-    for (int q = 0; q < 4; ++q) {
-      sm100::mbar_init(bar.tbl_free + 8 * q, 2);
-      sm100::mbar_init(bar.tbl_ready + 8 * q, 2);
-    }
     for (int s = 0; s < 2; ++s) {
+      sm100::mbar_init(bar.tbl_full + 8 * s, 1);
+      sm100::mbar_init(bar.tbl_empty + 8 * s, NDW);
       sm100::mbar_init(bar.acc_full + 8 * s, 1);
       sm100::mbar_init(bar.acc_empty + 8 * s, 2 * 4);
     }
@@ -232,7 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   sm100::tc_fence_before();
   sm100::cluster_sync();   // both CTAs' barriers initialised, tensor memory allocated, tiles counted
   sm100::tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + OFF_MISC);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_raw + OFF_MISC);
   const int nitems = cum[G] * a.ntl;
   auto tile_at = [&](int item) {
     Tile t;
@@ -254,18 +263,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     return t;
   };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ x producer
     const uint32_t lead_full = sm100::mapa_shared(bar.full_x, 0);
-    int it = 0;
+    int st = 0, turn = 0;                      // steps of warp 0 and of warp 3 alternate
+    uint32_t ph = 1;                           // a fresh barrier passes a wait for the phase before its first
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
       const Tile t = tile_at(wi);
       const int nr = t.nh / 2;                 // rows of this CTA per half
+      const int groups = nr / 4, boxes = (nr + X_BOX - 1) / X_BOX;
+      const int rows = a.g.x_rows ? nr : boxes * X_BOX;   // rows copied per half
+      // gathered: lane l takes rows 4 l .. 4 l + 3 of each half (nr <= 96: 24 lanes); a place past the tile or a
+      // row out of range reads row 0, whose column is not stored
+      int4 r[2];
       if (a.g.x_rows) {
-        // lane l gathers rows 4 l .. 4 l + 3 of each half (nr <= 96: 24 lanes); a place past the tile or
-        // a row out of range reads row 0, whose column is not stored
-        const int groups = nr / 4;
-        int4 r[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           int v[4];
@@ -278,242 +289,348 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           r[h] = make_int4(v[0], v[1], v[2], v[3]);
         }
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % SX;
-          if (it >= SX && !warp_wait(bar.empty_x + 8 * s, ((it / SX) & 1) ^ 1, true)) { ok = false; break; }
-          if (lead && lane == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * s, 2 * t.halves * nr * 128);
+      }
+      for (int sp = 0; sp < nst; ++sp) {
+        if (turn == (warp & 1)) {
+          const int blocks = min(2, nkb - 2 * sp);
+          if (!warp_wait(bar.empty_x + 8 * st, ph, false)) { ok = false; break; }
+          if (lead && lane == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
           __syncwarp();
-          if (lane < groups) {
-            const uint32_t dst = sbase + OFF_X + s * X_BYTES + lane * 512;
-            sm100::tma_gather4_pair(dst, &map_x, kb * 64, r[0], lead_full + 8 * s);
-            if (t.halves == 2) sm100::tma_gather4_pair(dst + (XR / 2) * 128, &map_x, kb * 64, r[1], lead_full + 8 * s);
+          const uint32_t dst = sbase + OFF_X + st * 2 * xblk, full = lead_full + 8 * st;
+          for (int b = 0; b < blocks; ++b) {
+            const int kx = (2 * sp + b) * 64;
+            if (a.g.x_rows) {
+              if (lane < groups) {
+                sm100::tma_gather4_pair(dst + b * xblk + lane * 512, &map_x, kx, r[0], full);
+                if (t.halves == 2) sm100::tma_gather4_pair(dst + b * xblk + nr * 128 + lane * 512, &map_x, kx, r[1], full);
+              }
+            } else if (lane < boxes * t.halves) {   // rows past the tile are other rows, whose columns are not stored
+              const int h = lane >= boxes, j = lane - (h ? boxes : 0);
+              sm100::tma_load_2d_pair(dst + b * xblk + (h * boxes + j) * X_BOX * 128, &map_x, kx,
+                                      t.p0 + h * t.nh + (int)rank * nr + j * X_BOX, full);
+            }
           }
         }
-      } else if (lane == 0) {
-        const int boxes = (nr + X_BOX - 1) / X_BOX;   // rows past the tile load other rows, whose columns are not stored
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % SX;
-          if (it >= SX && !wt.wait(bar.empty_x + 8 * s, ((it / SX) & 1) ^ 1, true)) { ok = false; break; }
-          if (lead) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * s, 2 * t.halves * boxes * X_BOX * 128);
-          for (int h = 0; h < t.halves; ++h)
-            for (int b = 0; b < boxes; ++b)
-              sm100::tma_load_2d_pair(sbase + OFF_X + s * X_BYTES + h * (XR / 2) * 128 + b * X_BOX * 128, &map_x, kb * 64,
-                                      t.p0 + h * t.nh + (int)rank * nr + b * X_BOX, lead_full + 8 * s);
+        turn ^= 1;
+        if (++st == a.xst) {
+          st = 0;
+          ph ^= 1;
         }
       }
     }
   } else if (warp == 1) {
-    if (lead && lane == 0) {
+    if (lead) {
       // ---------------------------------------------------------- MMA issuer (even CTA)
-      int it = 0;
+      int sx = 0, sa = 0;
+      uint32_t phx = 0, pha = 0;
       Slots sl;
+      const uint64_t xdesc = sm100::sw128_kmajor_desc(sbase + OFF_X);   // + address / 16 (below 2^14: no carry)
       for (int wi = pair; wi < nitems && ok; wi += npairs) {
         const Tile t = tile_at(wi);
         const int slots = a.nseg > 1 ? 2 : t.halves, first_slot = sl.take(slots);
-        for (int j = first_slot; j < first_slot + slots && ok; ++j)
-          if (sl.used[j] > 0 && !wt.wait(bar.acc_empty + 8 * j, (sl.used[j] - 1) & 1, true)) ok = false;
-        if (!ok) break;
+        if ((first_slot == 0 && sl.used0 > 0 && !warp_wait(bar.acc_empty, (sl.used0 - 1) & 1, true)) ||
+            (first_slot + slots == 2 && sl.used1 > 0 && !warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, true))) {
+          ok = false;
+          break;
+        }
         sm100::tc_fence_after();
         const uint32_t idesc = sm100::idesc_bf16_f32(256, t.nh);
-        const uint32_t d0 = tmem + D_COL + first_slot * NS;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int sx = it % SX, sa = it % SA;
-          if (!wt.wait(bar.full_x + 8 * sx, (it / SX) & 1, true) || !wt.wait(bar.dec_done + 8 * sa, (it / SA) & 1, false) ||
-              !wt.wait(bar.peer_a + 8 * sa, (it / SA) & 1, true)) {
-            ok = false;
-            break;
-          }
+        // the second half's x rows follow the first's (whole copies when they are not gathered)
+        const uint32_t half = (a.g.x_rows ? t.nh / 2 : (t.nh / 2 + X_BOX - 1) / X_BOX * X_BOX) * 128 >> 4;
+        uint32_t d0 = tmem + D_COL + first_slot * NS;
+        int left = a.seg;                      // steps left in this run
+        uint32_t add = 0;                      // 0 for the first MMA of a run, which overwrites
+        for (int sp = 0; sp < nst; ++sp) {
+          if (!warp_wait(bar.full_x + 8 * sx, phx, false) || !warp_wait(bar.ready_a + 8 * sa, pha, false)) { ok = false; break; }
           sm100::tc_fence_after();
-          const uint32_t at = tmem + A_COL + sa * 32, xb = sbase + OFF_X + sx * X_BYTES;
-          const int run = kb / a.seg;
-          const bool first = kb == run * a.seg;
-          for (int h = 0; h < t.halves; ++h) {
-            const uint32_t d = d0 + (a.nseg > 1 ? run * t.nh : h * NS);
+          const int blocks = min(2, nkb - 2 * sp);
+          if (sm100::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              sm100::mma_f16kind_pair_ts(d, at + kk * 8, sm100::sw128_kmajor_desc(xb + h * (XR / 2) * 128 + kk * 32), idesc,
-                                         (!first || kk > 0) ? 1u : 0u);
+            for (int b = 0; b < 2; ++b) {
+              if (b >= blocks) break;
+              const uint32_t at = tmem + A_COL + sa * 64 + b * 32;
+              const uint64_t bd = xdesc + ((sx * 2 + b) * xblk >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) sm100::mma_f16kind_pair_ts(d0, at + kk * 8, bd + 2 * kk, idesc, add | kk | b);
+              if (t.halves == 2) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  sm100::mma_f16kind_pair_ts(d0 + NS, at + kk * 8, bd + half + 2 * kk, idesc, add | kk | b);
+              }
+            }
+            sm100::mma_commit_pair(bar.empty_x + 8 * sx, PAIR);
+            sm100::mma_commit_pair(bar.empty_a + 8 * sa, PAIR);
           }
-          sm100::mma_commit_pair(bar.empty_x + 8 * sx, PAIR);
-          sm100::mma_commit_pair(bar.empty_a + 8 * sa, PAIR);
+          __syncwarp();
+          add = 1;
+          if (--left == 0) {                   // the next run has an accumulator of its own
+            left = a.seg;
+            add = 0;
+            d0 += t.nh;
+          }
+          if (++sx == a.xst) {
+            sx = 0;
+            phx ^= 1;
+          }
+          if (++sa == SA) {
+            sa = 0;
+            pha ^= 1;
+          }
         }
         if (!ok) break;
-        for (int j = first_slot; j < first_slot + slots; ++j) sm100::mma_commit_pair(bar.acc_full + 8 * j, PAIR);
+        if (sm100::elect_one()) {
+          if (first_slot == 0) sm100::mma_commit_pair(bar.acc_full, PAIR);
+          if (first_slot + slots == 2) sm100::mma_commit_pair(bar.acc_full + 8, PAIR);
+        }
+        __syncwarp();
         sl.done(first_slot, slots);
       }
-    } else if (!lead && lane == 0) {
-      // ---------------------------------------------------------- forwarder (odd CTA)
-      const uint32_t lead_peer = sm100::mapa_shared(bar.peer_a, 0);
-      int it = 0;
-      for (int wi = pair; wi < nitems && ok; wi += npairs)
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int sa = it % SA;
-          if (!wt.wait(bar.dec_done + 8 * sa, (it / SA) & 1, false)) {
-            ok = false;
-            break;
-          }
-          sm100::tc_fence_after();
-          sm100::tc_fence_before();
-          sm100::mbar_arrive_cluster(lead_peer + 8 * sa);
-        }
     }
   } else if (warp == 2) {
-    // ------------------------------------------------------------ code and table producer
-    if (lane == 0) {
-      int ic = 0, tl = 0;
-      const int ncs = (nkb + CKB - 1) / CKB;
-      const int64_t rows = (int64_t)G * a.N;
-      for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
-        const Tile t = tile_at(wi);
-        const int n0 = (t.wt * 2 + (int)rank) * (GATED ? RW / 2 : RW);
-        const int64_t row0 = (int64_t)t.g * a.N + n0;
-        if (tl > 0 && !wt.wait(bar.lut_empty, (tl - 1) & 1, false)) { ok = false; break; }
-        // rows past this group's last load the next group's (or none): their results are not stored
-        constexpr int per = GATED ? RW / 2 : RW;
-        const int have = n0 < a.N ? (int)min((int64_t)per, rows - row0) : 0;
-        if (have > 0) {
-          sm100::mbar_arrive_expect_tx(bar.lut_full, (GATED ? 2 : 1) * have * 128);
-          sm100::bulk_g2s(sbase + OFF_LUT, a.lut + row0 * 64, have * 128, bar.lut_full);
-          if (GATED) sm100::bulk_g2s(sbase + OFF_LUT + per * 128, a.lut2 + row0 * 64, have * 128, bar.lut_full);
-        } else {
-          sm100::mbar_arrive(bar.lut_full);
-        }
-        for (int cs = 0; cs < ncs; ++cs, ++ic) {
-          const int s = ic % SC;
-          if (ic >= SC && !wt.wait(bar.empty_c + 8 * s, ((ic / SC) & 1) ^ 1, false)) { ok = false; break; }
-          if (have > 0) {
-            const uint32_t dst = sbase + OFF_C + s * C_BYTES;
-            sm100::mbar_arrive_expect_tx(bar.full_c + 8 * s, C_BYTES);
-            sm100::tma_load_2d(dst, &map_c, cs * C_ROW, (int)row0, bar.full_c + 8 * s);
-            if (GATED) sm100::tma_load_2d(dst + C_BYTES / 2, &map_c2, cs * C_ROW, (int)row0, bar.full_c + 8 * s);
-          } else {
-            sm100::mbar_arrive(bar.full_c + 8 * s);
-          }
-        }
-      }
-    }
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------ decoders
-    const int q = warp & 3, wg = (warp >> 2) & 1;
-    // the row of the staged codes and tables that this lane decodes
-    const int row = GATED ? (lane < 16 ? 0 : RW / 2) + 16 * q + (lane & 15) : 32 * q + lane;
-    const uint32_t tbl = sbase + q * 8192 + lane * 4;
-    const uint32_t lutrow = sbase + OFF_LUT + row * 128;
-    int it = 0, ic = 0, tl = 0;
-    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
-      // the lane-private tables of this tile: each of the two warps of these rows writes half of them
-      if (!warp_wait(bar.lut_full, tl & 1, false)) { ok = false; break; }
-      uint32_t e[16];
+    // ------------------------------------------------------------ codes, and the next tile's tables
+    constexpr int per = GATED ? RW / 2 : RW;
+    const int ncs = (nkb + CKB - 1) / CKB;
+    int sc = 0, tl = 0, q = 4;                 // q: the next quarter of the tables to load; 4: none
+    uint32_t phc = 1;
+    Tile nx{};                                 // the tile that the tables are for
+    uint4 e[8];
+    // one quarter: lane l's row's 64 entries, then word c * 32 + l of the buffer for entry c
+    auto load = [&]() {
+      const int r = (nx.wt * 2 + (int)rank) * per + (GATED ? 16 * q + (lane & 15) : 32 * q + lane);
+      const uint16_t *src = (GATED && lane >= 16 ? a.lut2 : a.lut) + ((size_t)nx.g * a.N + min(r, a.N - 1)) * 64;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) lds128(lutrow + wg * 64 + ((j + lane) & 3) * 16, e[4 * j], e[4 * j + 1], e[4 * j + 2], e[4 * j + 3]);
-      __syncwarp();
-      if (lane == 0) {
-        sm100::mbar_arrive(bar.lut_empty);
-        sm100::mbar_arrive(bar.tbl_free + 8 * q);
-      }
-      if (!warp_wait(bar.tbl_free + 8 * q, tl & 1, false)) { ok = false; break; }   // both warps are past the last tile
+      for (int j = 0; j < 8; ++j) e[j] = __ldg(reinterpret_cast<const uint4 *>(src) + j);
+    };
+    auto store = [&](int b) {
+      const uint32_t to = sbase + b * TBL_BYTES + q * 8192 + lane * 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t to = tbl + (wg * 32 + ((j + lane) & 3) * 8) * 128;
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t u[4] = {e[j].x, e[j].y, e[j].z, e[j].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sts32(to + 2 * i * 128, e[4 * j + i] & 0xffffu);
-          sts32(to + (2 * i + 1) * 128, e[4 * j + i] >> 16);
+          sts32(to + (8 * j + 2 * i) * 128, u[i] & 0xffffu);
+          sts32(to + (8 * j + 2 * i + 1) * 128, u[i] >> 16);
         }
       }
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(bar.tbl_ready + 8 * q);
-      if (!warp_wait(bar.tbl_ready + 8 * q, tl & 1, false)) { ok = false; break; }
-
-      for (int kb0 = 0; kb0 < nkb && ok; kb0 += CKB, ++ic) {
-        const int sc = ic % SC;
-        if (!warp_wait(bar.full_c + 8 * sc, (ic / SC) & 1, false)) { ok = false; break; }
-        const int kb1 = min(nkb, kb0 + CKB);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          if ((it & 1) != wg) continue;
-          uint32_t w[12];
-          const uint32_t cp = sbase + OFF_C + sc * C_BYTES + row * C_ROW + (kb - kb0) * 48;
+      if (++q < 4) {
+        load();
+      } else {
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(bar.tbl_full + 8 * b);
+      }
+    };
+    if (pair < nitems) {                       // the first tile's tables
+      nx = tile_at(pair);
+      q = 0;
+      load();
+      while (q < 4) store(0);
+    }
+    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
+      const Tile t = nx;
+      const int n0 = (t.wt * 2 + (int)rank) * per;
+      const int row0 = t.g * a.N + n0;         // rows past this group's last are the next group's: results not stored
+      const int b = (tl + 1) & 1;              // the next tile's table buffer
+      if (wi + npairs < nitems) {
+        nx = tile_at(wi + npairs);
+        q = 0;
+        load();
+      }
+      for (int cs = 0; cs < ncs; ++cs) {
+        if (!warp_wait(bar.empty_c + 8 * sc, phc, false)) { ok = false; break; }
+        if (sm100::elect_one()) {
+          if (n0 < a.N) {
+            const uint32_t dst = sbase + OFF_C + sc * C_BYTES;
+            sm100::mbar_arrive_expect_tx(bar.full_c + 8 * sc, C_BYTES);
+            sm100::tma_load_2d(dst, &map_c, cs * C_ROW, row0, bar.full_c + 8 * sc);
+            if (GATED) sm100::tma_load_2d(dst + C_BYTES / 2, &map_c2, cs * C_ROW, row0, bar.full_c + 8 * sc);
+          } else {
+            sm100::mbar_arrive(bar.full_c + 8 * sc);
+          }
+        }
+        __syncwarp();
+        if (++sc == SC) {
+          sc = 0;
+          phc ^= 1;
+        }
+        // Past SC stages the decoders are on this tile, so the buffer of the one before is free.
+        if (q < 4 && cs >= SC) {
+          if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, false)) { ok = false; break; }
+          store(b);
+        }
+      }
+      if (ok && q < 4) {
+        if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, false)) ok = false;
+        while (ok && q < 4) store(b);
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ decoders
+    const int q = warp & 3, wg = (warp >> 2) & 1;
+    // the row of the staged codes that this lane decodes
+    const int row = GATED ? (lane < 16 ? 0 : RW / 2) + 16 * q + (lane & 15) : 32 * q + lane;
+    const uint32_t lead_ready = sm100::mapa_shared(bar.ready_a, 0);
+    int tl = 0, sa = 0, sc = 0;
+    uint32_t pha = 1, phc = 0;
+    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
+      const uint32_t tbl = sbase + (tl & 1) * TBL_BYTES + q * 8192 + lane * 4;
+      if (!warp_wait(bar.tbl_full + 8 * (tl & 1), (tl >> 1) & 1, false)) { ok = false; break; }
+      int sub = -1;                            // K block within the code stage; -1: the stage has not been waited for
+      for (int sp = 0; sp < nst; ++sp) {
+        const bool live = 2 * sp + wg < nkb;
+        uint32_t out[32];
+        // this warpgroup's K block of the step, past the other's
+        for (int b = 0; b < 2 && ok; ++b) {
+          if (2 * sp + b >= nkb) break;
+          if (sub < 0) {
+            if (!warp_wait(bar.full_c + 8 * sc, phc, false)) { ok = false; break; }
+            sub = 0;
+          }
+          if (b == wg) {
+            uint32_t w[12];
+            const uint32_t cp = sbase + OFF_C + sc * C_BYTES + row * C_ROW + sub * 48;
 #pragma unroll
-          for (int j = 0; j < 3; ++j) lds128(cp + 16 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          uint32_t out[32];
-          Lookup<64>::run(w, tbl, out);
-          const int sa = it % SA;
-          if (it >= SA && !warp_wait(bar.empty_a + 8 * sa, ((it / SA) & 1) ^ 1, true)) { ok = false; break; }
+            for (int j = 0; j < 3; ++j) lds128(cp + 16 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            Lookup<64>::run(w, tbl, out);
+          }
+          if (++sub == CKB || 2 * sp + b + 1 == nkb) {   // the stage's last K block
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(bar.empty_c + 8 * sc);
+            sub = -1;
+            if (++sc == SC) {
+              sc = 0;
+              phc ^= 1;
+            }
+          }
+        }
+        if (!ok) break;
+        if (!warp_wait(bar.empty_a + 8 * sa, pha, false)) { ok = false; break; }
+        if (live) {
           sm100::tc_fence_after();
-          __syncwarp();
-          sm100::tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + A_COL + sa * 32, out);
+          sm100::tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + A_COL + sa * 64 + wg * 32, out);
           sm100::tmem_wait_st();
           sm100::tc_fence_before();
           __syncwarp();
-          if (lane == 0) sm100::mbar_arrive(bar.dec_done + 8 * sa);
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(bar.empty_c + 8 * sc);
+        if (lane == 0) sm100::mbar_arrive_cluster_relaxed(lead_ready + 8 * sa);
+        if (++sa == SA) {
+          sa = 0;
+          pha ^= 1;
+        }
       }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(bar.tbl_empty + 8 * (tl & 1));
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    const int q = warp & 3, es = (warp - 4) >> 2;   // this warp's lanes of tensor memory, and its slot
     const uint32_t lead_empty = sm100::mapa_shared(bar.acc_empty, 0);
     Slots sl;
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
       const Tile t = tile_at(wi);
-      const int slots = a.nseg > 1 ? 2 : t.halves, first_slot = sl.take(slots);
+      const bool runs = a.nseg > 1;            // both slots hold one tile's runs; its 16-column chunks alternate
+      const int slots = runs ? 2 : t.halves, first_slot = sl.take(slots), used0 = sl.used0, used1 = sl.used1;
+      sl.done(first_slot, slots);
+      if (slots == 1 && es != first_slot) continue;
       const int n = GATED ? (t.wt * 2 + (int)rank) * (RW / 2) + 16 * q + (lane & 15)
                           : (t.wt * 2 + (int)rank) * RW + 32 * q + lane;
-      for (int h = 0; h < t.halves && ok; ++h) {
-        const int slot = first_slot + h;
-        if (!warp_wait(bar.acc_full + 8 * slot, sl.used[slot] & 1, true)) { ok = false; break; }
-        if (a.nseg > 1 && !warp_wait(bar.acc_full + 8, sl.used[1] & 1, true)) { ok = false; break; }
-        sm100::tc_fence_after();
+      const int pbase = t.p0 + (t.halves == 2 ? es * t.nh : 0);
+      // the output row of position pbase + c + (lane & 15), -1 for none
+      auto row_of = [&](int c) {
+        const int p = pbase + c + (lane & 15);
+        if (c >= t.nh || p >= t.p1) return -1;
+        const int yr = a.g.y_rows ? __ldcg(a.g.y_rows + p) : p, xi = a.g.x_rows ? __ldcg(a.g.x_rows + p) : p;
+        return (unsigned)yr >= (unsigned)a.g.Y || xi < 0 || (a.g.x_rows ? xi / a.g.x_div : xi) >= a.g.X ? -1 : yr;
+      };
+      const int c0 = runs ? 16 * es : 0, step = runs ? 32 : 16;
+      int next = row_of(c0);
+      if (!warp_wait(bar.acc_full + 8 * es, (es ? used1 : used0) & 1, true) ||
+          (runs && !warp_wait(bar.acc_full + 8 * (es ^ 1), (es ? used0 : used1) & 1, true))) {
+        ok = false;
+        break;
+      }
+      sm100::tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + D_COL + (runs ? 0 : es * NS);
+      if (a.vec) {
+        // bf16 rows of 8-feature pieces: fragments of 16 lanes (features) x 16 columns (positions), transposed on
+        // their way through this warp's own kilobyte of shared memory, leave as 16-byte stores.  One store and a
+        // half per 8 columns instead of 8 shuffles and 8 two-byte stores: those queue behind the decoders' lookups.
+        constexpr int FW = GATED ? 16 : 32;    // features of this warp
+        const uint32_t stg = sbase + OFF_STG + (warp - 4) * STG_BYTES;
+        // matrices of 8 features x 8 positions, thread i giving row i % 8 (a position) of matrix i / 8.  The 16-byte
+        // pieces of a position are permuted so that 8 positions share no bank.
+        constexpr int PP = FW / 8, NP = 32 / PP;   // 16-byte pieces per position, positions per round
+        auto piece = [&](int pos, int f8) {
+          return stg + pos * (FW * 2) + ((f8 ^ (GATED ? (pos >> 2) & 1 : (pos >> 1) & 3)) << 4);
+        };
+        const int mpos = GATED ? (lane & 7) + ((lane >> 4) << 3) : lane & 7, mf = GATED ? (lane >> 3) & 1 : lane >> 3;
+        const int nb = (t.wt * 2 + (int)rank) * (GATED ? RW / 2 : RW) + FW * q;   // this warp's first feature
         for (int c = 0; c < t.nh; c += 16) {
-          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + D_COL + slot * NS + c;
-          uint32_t v[16];
-          sm100::tmem_ld_32x32b_x16(at, v);
+          uint32_t lo[8], hi[8];               // lanes 0-15 and 16-31 of this warp's quarter
+          sm100::tmem_ld_16x256b_x2(acc + c, lo);
+          sm100::tmem_ld_16x256b_x2(acc + c + (16u << 16), hi);
+          const int yr = next;
+          next = row_of(c + 16);
           sm100::tmem_wait_ld();
-          for (int r = 1; r < a.nseg; ++r) {
-            uint32_t u[16];
-            sm100::tmem_ld_32x32b_x16(at + r * t.nh, u);
-            sm100::tmem_wait_ld();
+          if constexpr (GATED) {               // lo is g and hi is u of the same features and positions
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+            for (int i = 0; i < 8; ++i) lo[i] = __float_as_uint(qld::silu_mul(__uint_as_float(lo[i]), __uint_as_float(hi[i])));
           }
-          // the output row of position c + (lane & 15), -1 for none
-          const int p = t.p0 + h * t.nh + c + (lane & 15);
-          int yr = -1;
-          if (p < t.p1) {
-            yr = a.g.y_rows ? __ldcg(a.g.y_rows + p) : p;
-            const int xi = a.g.x_rows ? __ldcg(a.g.x_rows + p) : p;
-            if ((unsigned)yr >= (unsigned)a.g.Y || xi < 0 || (a.g.x_rows ? xi / a.g.x_div : xi) >= a.g.X) yr = -1;
-          }
-          if constexpr (GATED) {
-            // lanes 0-15 hold g, lanes 16-31 u of the same features: after the exchange the lower half has both
-            // for columns 0-7 and the upper half for columns 8-15
+          auto two = [&](const uint32_t(&v)[8], int i) { return pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), OUT_BF16); };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t mine = lane < 16 ? v[i] : v[8 + i], give = lane < 16 ? v[8 + i] : v[i];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 16);
-              const float gv = __uint_as_float(lane < 16 ? mine : got), uv = __uint_as_float(lane < 16 ? got : mine);
-              const int yi = __shfl_sync(0xffffffffu, yr, (lane < 16 ? 0 : 8) + i);
-              if (yi >= 0 && n < a.N) store_out(a.y, a.ydt, (size_t)yi * a.N + n, qld::silu_mul(gv, uv));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int yi = __shfl_sync(0xffffffffu, yr, i);
-              if (yi >= 0 && n < a.N) store_out(a.y, a.ydt, (size_t)yi * a.N + n, __uint_as_float(v[i]));
-            }
+          for (int r = 0; r < 16 / NP; ++r) {
+            __syncwarp();                      // the last round has been read out of the staging
+            if constexpr (GATED)
+              sm100::stmatrix_x4_trans(piece(mpos, mf), two(lo, 0), two(lo, 2), two(lo, 4), two(lo, 6));
+            else
+              sm100::stmatrix_x4_trans(piece(mpos, mf), two(lo, 4 * r), two(lo, 4 * r + 2), two(hi, 4 * r), two(hi, 4 * r + 2));
+            __syncwarp();
+            const int pos = lane / PP, f8 = lane % PP;
+            const int yi = __shfl_sync(0xffffffffu, yr, NP * r + pos);
+            uint32_t x0, x1, x2, x3;
+            lds128(piece(pos, f8), x0, x1, x2, x3);
+            if (yi >= 0 && nb + 8 * f8 < a.N)
+              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + (size_t)yi * a.N + nb + 8 * f8) =
+                  make_uint4(x0, x1, x2, x3);
           }
         }
-        sm100::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          sm100::mbar_arrive_cluster(lead_empty + 8 * slot);
-          if (a.nseg > 1) sm100::mbar_arrive_cluster(lead_empty + 8);
+      } else {
+      for (int c = c0; c < t.nh; c += step) {
+        uint32_t v[16];
+        sm100::tmem_ld_32x32b_x16(acc + c, v);
+        const int yr = next;
+        next = row_of(c + step);
+        sm100::tmem_wait_ld();
+        for (int r = 1; r < a.nseg; ++r) {
+          uint32_t u[16];
+          sm100::tmem_ld_32x32b_x16(acc + c + r * t.nh, u);
+          sm100::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+        }
+        if constexpr (GATED) {
+          // lanes 0-15 hold g, lanes 16-31 u of the same features: after the exchange the lower half has both
+          // for columns 0-7 and the upper half for columns 8-15
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t mine = lane < 16 ? v[i] : v[8 + i], give = lane < 16 ? v[8 + i] : v[i];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 16);
+            const float gv = __uint_as_float(lane < 16 ? mine : got), uv = __uint_as_float(lane < 16 ? got : mine);
+            const int yi = __shfl_sync(0xffffffffu, yr, (lane < 16 ? 0 : 8) + i);
+            if (yi >= 0 && n < a.N) store_out(a.y, a.ydt, (size_t)yi * a.N + n, qld::silu_mul(gv, uv));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int yi = __shfl_sync(0xffffffffu, yr, i);
+            if (yi >= 0 && n < a.N) store_out(a.y, a.ydt, (size_t)yi * a.N + n, __uint_as_float(v[i]));
+          }
         }
       }
-      sl.done(first_slot, slots);
+      }
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive_cluster_relaxed(lead_empty + 8 * es);
     }
   }
 
@@ -540,7 +657,7 @@ int resident_pairs() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (ql::sm_count() / 2));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes(QL_MAX_GROUPS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, benq_grouped_kernel<GATED>, &cfg) != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
@@ -562,7 +679,7 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return fail(QL_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", who);
   const int per = codes2 ? RW / 2 : RW;   // rows of each layer per CTA and tile
-  CUtensorMap mx, mc, mc2;
+  CUtensorMap mx;
   if (!encode_rows_sw128(enc, &mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, g.X, K, K, g.x_rows ? 1 : X_BOX))
     return fail(QL_ERR_CUDA, "%s: cannot encode the activation tensor map", who);
   auto codes_map = [&](CUtensorMap *m, const uint8_t *c) {
@@ -575,23 +692,31 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
+  CUtensorMap mc, mc2;
   if (!codes_map(&mc, codes) || !codes_map(&mc2, codes2 ? codes2 : codes))
     return fail(QL_ERR_CUDA, "%s: cannot encode the code tensor map", who);
-  Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), NT, K / 64, 1};
-  if (ydt == QL_OUT_F32 && K / 64 > SEG_KB) {
-    a.seg = std::max(SEG_KB, (K / 64 + MAX_SEG - 1) / MAX_SEG);
-    a.nseg = (K / 64 + a.seg - 1) / a.seg;
-    a.nt_max = std::min(NS, NT / a.nseg / 16 * 16);   // every run's accumulator fits beside the others
+  Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), 0, 0, 0, ydt == QL_OUT_BF16 && N % 8 == 0, K, 1};
+  // Positions per tile: room for a group of four times the average length, so that few groups take a second pass
+  // over their codes, and no more than that, because shorter x stages are more of them.
+  const int want = std::max(1, (int)std::min<int64_t>(4LL * (g.M / g.G), NT));
+  auto room = [](int n) { return n <= NS ? (n + 63) / 64 * 64 : (n + 127) / 128 * 128; };   // 64, 128, 192, 256, 384
+  a.nt_max = room(want);
+  const int steps = (K / 64 + 1) / 2;
+  if (ydt == QL_OUT_F32 && steps > SEG_STEPS) {
+    a.seg = std::max(SEG_STEPS, (steps + MAX_SEG - 1) / MAX_SEG);
+    a.nseg = (steps + a.seg - 1) / a.seg;
+    a.nt_max = std::min({a.nt_max, NS, NT / a.nseg / 16 * 16});   // every run's accumulator fits beside the others
   }
-  const size_t smem = smem_bytes(g.G);
+  a.xr = room(a.nt_max) / 2;
+  a.xst = std::min(SX_MAX, X_RING / (2 * a.xr * 128));
   // the most tiles that the counts could make (each group may end inside a tile)
   const int64_t items = ((int64_t)std::min(g.G, g.M) + g.M / a.nt_max) * a.ntl;
   auto go = [&](auto gated) -> ql_status {
     constexpr bool GATED = decltype(gated)::value;
-    if (set_max_smem(benq_grouped_kernel<GATED>, (int)smem_bytes(QL_MAX_GROUPS)) != cudaSuccess)
+    if (set_max_smem(benq_grouped_kernel<GATED>, SMEM_BYTES) != cudaSuccess)
       return fail(QL_ERR_CUDA, "%s: cannot reserve shared memory", who);
     const int grid = 2 * (int)std::min<int64_t>(items, resident_pairs<GATED>());
-    launch(benq_grouped_kernel<GATED>, grid, THREADS, smem, s, mx, mc, mc2, a);
+    launch(benq_grouped_kernel<GATED>, grid, THREADS, SMEM_BYTES, s, mx, mc, mc2, a);
     return launch_status(who);
   };
   return codes2 ? go(std::true_type{}) : go(std::false_type{});

@@ -15,10 +15,10 @@
 // Per 64-wide K block and SM that is 256 + 48 wavefronts of lookups and codes, 48 of code writes and
 // n/2 + n/2 of X for n positions, against 2 n clocks of MMA.
 //
-// Roles (640 threads per CTA): warps 0 and 3 load X on alternate steps (rows gathered by x_rows: a gather of four rows
-// takes about 40 clocks to issue, or tiles); warp 1 issues the MMAs (even CTA); warp 2 loads codes and, between them,
-// lays out the next tile's tables; warps 4-7 and 8-11 drain the accumulator slots 0 and 1; warps 12-19, two
-// warpgroups, decode the two K blocks of a step.  Accumulators are two
+// Roles (768 threads per CTA): warps 0 and 3 load X on alternate steps (rows gathered by x_rows, or tiles); warp 1
+// issues the MMAs (even CTA); warp 2 loads codes and, between them, lays out the next tile's tables; warps 4-7 drain
+// the accumulators; warps 8-23, four warpgroups, decode: two to a step of two K blocks, in turn, because a warp's
+// waits and hand-over take as long as its lookups (two warpgroups left the port idle half of the time).  Accumulators are two
 // slots of 192 columns, so one tile's epilogue overlaps the next tile's MMAs.  The decoders of the odd CTA arrive at
 // the even CTA's barrier with relaxed semantics: what they hand over is in tensor memory, which the tcgen05 fences
 // order (a cluster-scope release by one relaying thread took 1300 clocks per K block and set the kernel's pace).
@@ -50,12 +50,11 @@ constexpr int SA = 2, SC = 3;                  // stages: decoded W (steps), cod
 constexpr int X_RING = 96 * 1024;              // x stages of one step each: two 64-column blocks of half a tile's rows
 constexpr int SX_MAX = 8;
 constexpr int X_BOX = 32;                      // rows per copy when rows are not gathered
-constexpr int CKB = 3;                         // K blocks per code stage: rows of 144 bytes, so that a 16-byte load
-constexpr int C_ROW = CKB * 48;                // of 8 rows at a time is free of bank conflicts
-constexpr int C_BYTES = RW * C_ROW;            // 18 KB
+constexpr int C_LINE = 128;                    // code bytes per row and stage: 128-byte rows in the 128-byte swizzle.  (Unswizzled
+constexpr int C_BYTES = RW * C_LINE;           // 144-byte rows, three K blocks, took the TMA unit 21 clocks each.)  16 KB
 constexpr int TBL_BYTES = 4 * 8192;            // lane-private tables: 4 warps of rows x [64][32] words, two buffers
-constexpr int NDW = 8;                         // decoder warps (two warpgroups)
-constexpr int THREADS = 640;
+constexpr int NDW = 16;                        // decoder warps: four warpgroups, two per step in turn
+constexpr int THREADS = (8 + NDW) * 32;
 constexpr int D_COL = 0, A_COL = NT;           // tensor memory columns: accumulators, then SA steps of 2 x 32
 constexpr int MAX_SEG = NT / 16;               // runs of K blocks with an accumulator each (fp32 outputs)
 constexpr int SEG_STEPS = 4;                   // 512 inputs
@@ -68,12 +67,14 @@ constexpr int OFF_MISC = NBAR * 8;             // tensor-memory address, abort f
 constexpr int OFF_GRP = OFF_MISC + 16;         // token tiles before each group, int [G + 1]
 constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
 constexpr int OFF_C = OFF_X + X_RING;
-constexpr int STG_BYTES = 512;                 // per epilogue warp: 8 positions x 32 features of bf16, or 16 x 16
+constexpr int STG_BYTES = 1024;                // per epilogue warp: 16 positions x 32 features of bf16
 constexpr int OFF_STG = OFF_C + SC * C_BYTES;
-constexpr int SMEM_BYTES = FRONT + OFF_STG + 8 * STG_BYTES;
+constexpr int OFF_ROW = OFF_STG + 4 * STG_BYTES;      // per x warp: the gathered rows of its tile, int [NS]
+constexpr int OFF_YROW = OFF_ROW + 2 * NS * 4;        // per epilogue warp: the output rows of a slot, int [NS]
+constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * NS * 4;
 static_assert(OFF_GRP + (QL_MAX_GROUPS + 1) * 4 <= FRONT, "front");
 static_assert(A_COL + 64 * SA <= 512, "tensor memory");
-static_assert(OFF_X % 1024 == 0 && OFF_C % 128 == 0 && C_BYTES % 128 == 0 && OFF_STG % 128 == 0, "alignment");
+static_assert(OFF_X % 1024 == 0 && OFF_C % 128 == 0 && C_BYTES % 1024 == 0 && OFF_C % 1024 == 0 && OFF_STG % 128 == 0, "alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr uint16_t PAIR = 0x3;
 
@@ -149,6 +150,10 @@ __device__ __forceinline__ void lds128(uint32_t a, uint32_t &x, uint32_t &y, uin
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(a));
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0], %1; }" ::"r"(bar), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ void store_out(void *y, int ydt, size_t i, float v) {
   if (ydt == QL_OUT_F32)
     static_cast<float *>(y)[i] = v;
@@ -192,12 +197,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       sm100::mbar_init(bar.empty_x + 8 * s, 1);
     }
     for (int s = 0; s < SA; ++s) {
-      sm100::mbar_init(bar.ready_a + 8 * s, 2 * NDW);   // the decoder warps of both CTAs
+      sm100::mbar_init(bar.ready_a + 8 * s, NDW);       // half of the decoder warps of both CTAs
       sm100::mbar_init(bar.empty_a + 8 * s, 1);
     }
     for (int s = 0; s < SC; ++s) {
       sm100::mbar_init(bar.full_c + 8 * s, 1);
-      sm100::mbar_init(bar.empty_c + 8 * s, NDW);
+      sm100::mbar_init(bar.empty_c + 8 * s, 4 * 4);     // four K blocks' warps
     }
     for (int s = 0; s < 2; ++s) {
       sm100::mbar_init(bar.tbl_full + 8 * s, 1);
@@ -273,22 +278,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int nr = t.nh / 2;                 // rows of this CTA per half
       const int groups = nr / 4, boxes = (nr + X_BOX - 1) / X_BOX;
       const int rows = a.g.x_rows ? nr : boxes * X_BOX;   // rows copied per half
-      // gathered: lane l takes rows 4 l .. 4 l + 3 of each half (nr <= 96: 24 lanes); a place past the tile or a
-      // row out of range reads row 0, whose column is not stored
-      int4 r[2];
+      // gathered rows: both halves' lists one after the other; a place past the tile or a row out of range reads row
+      // 0, whose column is not stored
+      const uint32_t list = sbase + OFF_ROW + (warp & 1) * NS * 4;
       if (a.g.x_rows) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int p = t.p0 + h * t.nh + (int)rank * nr + 4 * lane + e;
-            int x = 0;
-            if (h < t.halves && lane < groups && p < t.p1) x = __ldcg(a.g.x_rows + p) / a.g.x_div;
-            v[e] = (unsigned)x < (unsigned)a.g.X ? x : 0;
-          }
-          r[h] = make_int4(v[0], v[1], v[2], v[3]);
+        __syncwarp();
+        for (int i = lane; i < t.halves * nr; i += 32) {
+          const int h = i >= nr, p = t.p0 + h * t.nh + (int)rank * nr + i - (h ? nr : 0);
+          int x = 0;
+          if (p < t.p1) x = __ldcg(a.g.x_rows + p) / a.g.x_div;
+          sts32(list + 4 * i, (unsigned)x < (unsigned)a.g.X ? x : 0);
         }
+        __syncwarp();
       }
       for (int sp = 0; sp < nst; ++sp) {
         if (turn == (warp & 1)) {
@@ -297,19 +298,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (lead && lane == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
           __syncwarp();
           const uint32_t dst = sbase + OFF_X + st * 2 * xblk, full = lead_full + 8 * st;
-          for (int b = 0; b < blocks; ++b) {
-            const int kx = (2 * sp + b) * 64;
-            if (a.g.x_rows) {
-              if (lane < groups) {
-                sm100::tma_gather4_pair(dst + b * xblk + lane * 512, &map_x, kx, r[0], full);
-                if (t.halves == 2) sm100::tma_gather4_pair(dst + b * xblk + nr * 128 + lane * 512, &map_x, kx, r[1], full);
+          const int kx = 2 * sp * 64;
+          if (a.g.x_rows) {
+            if (sm100::elect_one()) {
+              // four lists at a time are loaded before their copies are issued: a load's latency per copy, in the queue
+              // behind the lookups, made a gather take 40 clocks
+              const int n4 = t.halves * groups;
+              for (int i0 = 0; i0 < n4; i0 += 4) {
+                uint32_t r[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lds128(list + 16 * (i0 + i), r[i][0], r[i][1], r[i][2], r[i][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (i0 + i >= n4) break;
+                  const int4 y = make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]);
+                  const uint32_t to = dst + (i0 + i) * 512;
+                  sm100::tma_gather4_pair(to, &map_x, kx, y, full);
+                  if (blocks == 2) sm100::tma_gather4_pair(to + xblk, &map_x, kx + 64, y, full);
+                }
               }
-            } else if (lane < boxes * t.halves) {   // rows past the tile are other rows, whose columns are not stored
-              const int h = lane >= boxes, j = lane - (h ? boxes : 0);
-              sm100::tma_load_2d_pair(dst + b * xblk + (h * boxes + j) * X_BOX * 128, &map_x, kx,
-                                      t.p0 + h * t.nh + (int)rank * nr + j * X_BOX, full);
             }
+            __syncwarp();
+          } else if (sm100::elect_one()) {      // rows past the tile are other rows, whose columns are not stored
+            for (int h = 0; h < t.halves; ++h)
+              for (int j = 0; j < boxes; ++j) {
+                const uint32_t to = dst + (h * boxes + j) * X_BOX * 128;
+                const int y = t.p0 + h * t.nh + (int)rank * nr + j * X_BOX;
+                sm100::tma_load_2d_pair(to, &map_x, kx, y, full);
+                if (blocks == 2) sm100::tma_load_2d_pair(to + xblk, &map_x, kx + 64, y, full);
+              }
           }
+          __syncwarp();
         }
         turn ^= 1;
         if (++st == a.xst) {
@@ -328,8 +347,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int wi = pair; wi < nitems && ok; wi += npairs) {
         const Tile t = tile_at(wi);
         const int slots = a.nseg > 1 ? 2 : t.halves, first_slot = sl.take(slots);
+        // a tile of two slots waits for the second one when its first step has multiplied into the first
+        const bool wait1 = first_slot + slots == 2 && sl.used1 > 0, late1 = t.halves == 2;
         if ((first_slot == 0 && sl.used0 > 0 && !warp_wait(bar.acc_empty, (sl.used0 - 1) & 1, true)) ||
-            (first_slot + slots == 2 && sl.used1 > 0 && !warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, true))) {
+            (wait1 && !late1 && !warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, true))) {
           ok = false;
           break;
         }
@@ -344,20 +365,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (!warp_wait(bar.full_x + 8 * sx, phx, false) || !warp_wait(bar.ready_a + 8 * sa, pha, false)) { ok = false; break; }
           sm100::tc_fence_after();
           const int blocks = min(2, nkb - 2 * sp);
-          if (sm100::elect_one()) {
+          const uint32_t at0 = tmem + A_COL + sa * 64;
+          const uint64_t bd0 = xdesc + (sx * 2 * xblk >> 4);
+          auto mmas = [&](uint32_t d, uint64_t bd) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               if (b >= blocks) break;
-              const uint32_t at = tmem + A_COL + sa * 64 + b * 32;
-              const uint64_t bd = xdesc + ((sx * 2 + b) * xblk >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) sm100::mma_f16kind_pair_ts(d0, at + kk * 8, bd + 2 * kk, idesc, add | kk | b);
-              if (t.halves == 2) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  sm100::mma_f16kind_pair_ts(d0 + NS, at + kk * 8, bd + half + 2 * kk, idesc, add | kk | b);
-              }
+              for (int kk = 0; kk < 4; ++kk)
+                sm100::mma_f16kind_pair_ts(d, at0 + b * 32 + kk * 8, bd + (b * xblk >> 4) + 2 * kk, idesc, add | kk | b);
             }
+          };
+          if (sm100::elect_one()) mmas(d0, bd0);
+          __syncwarp();
+          if (t.halves == 2) {
+            if (sp == 0 && wait1) {
+              if (!warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, true)) { ok = false; break; }
+              sm100::tc_fence_after();
+            }
+            if (sm100::elect_one()) mmas(d0 + NS, bd0 + half);
+            __syncwarp();
+          }
+          if (sm100::elect_one()) {
             sm100::mma_commit_pair(bar.empty_x + 8 * sx, PAIR);
             sm100::mma_commit_pair(bar.empty_a + 8 * sa, PAIR);
           }
@@ -389,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 2) {
     // ------------------------------------------------------------ codes, and the next tile's tables
     constexpr int per = GATED ? RW / 2 : RW;
-    const int ncs = (nkb + CKB - 1) / CKB;
+    const int nln = (48 * nkb + C_LINE - 1) / C_LINE;
     int sc = 0, tl = 0, q = 4;                 // q: the next quarter of the tables to load; 4: none
     uint32_t phc = 1;
     Tile nx{};                                 // the tile that the tables are for
@@ -435,14 +464,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         q = 0;
         load();
       }
-      for (int cs = 0; cs < ncs; ++cs) {
+      for (int ln = 0; ln < nln; ++ln) {
         if (!warp_wait(bar.empty_c + 8 * sc, phc, false)) { ok = false; break; }
         if (sm100::elect_one()) {
           if (n0 < a.N) {
             const uint32_t dst = sbase + OFF_C + sc * C_BYTES;
             sm100::mbar_arrive_expect_tx(bar.full_c + 8 * sc, C_BYTES);
-            sm100::tma_load_2d(dst, &map_c, cs * C_ROW, row0, bar.full_c + 8 * sc);
-            if (GATED) sm100::tma_load_2d(dst + C_BYTES / 2, &map_c2, cs * C_ROW, row0, bar.full_c + 8 * sc);
+            sm100::tma_load_2d(dst, &map_c, ln * C_LINE, row0, bar.full_c + 8 * sc);
+            if (GATED) sm100::tma_load_2d(dst + C_BYTES / 2, &map_c2, ln * C_LINE, row0, bar.full_c + 8 * sc);
           } else {
             sm100::mbar_arrive(bar.full_c + 8 * sc);
           }
@@ -453,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           phc ^= 1;
         }
         // Past SC stages the decoders are on this tile, so the buffer of the one before is free.
-        if (q < 4 && cs >= SC) {
+        if (q < 4 && ln >= SC) {
           if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, false)) { ok = false; break; }
           store(b);
         }
@@ -463,59 +492,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         while (ok && q < 4) store(b);
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ decoders
-    const int q = warp & 3, wg = (warp >> 2) & 1;
+    const int q = warp & 3, wg = (warp >> 2) - 2;
     // the row of the staged codes that this lane decodes
     const int row = GATED ? (lane < 16 ? 0 : RW / 2) + 16 * q + (lane & 15) : 32 * q + lane;
-    const uint32_t lead_ready = sm100::mapa_shared(bar.ready_a, 0);
-    int tl = 0, sa = 0, sc = 0;
-    uint32_t pha = 1, phc = 0;
-    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
+    const uint32_t crow = sbase + OFF_C + row * C_LINE;
+    const int sa = wg >> 1;                    // the stage of decoded W that this warpgroup writes, one of its two K blocks
+    const uint32_t ready = sm100::mapa_shared(bar.ready_a + 8 * sa, 0);
+    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + A_COL + sa * 64 + (wg & 1) * 32;
+    const int nln = (3 * nkb + 7) / 8;
+    int tl = 0;
+    uint32_t line0 = 0, step0 = 0;             // lines and steps of the tiles before
+    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl, line0 += nln, step0 += nst) {
       const uint32_t tbl = sbase + (tl & 1) * TBL_BYTES + q * 8192 + lane * 4;
       if (!warp_wait(bar.tbl_full + 8 * (tl & 1), (tl >> 1) & 1, false)) { ok = false; break; }
-      int sub = -1;                            // K block within the code stage; -1: the stage has not been waited for
-      for (int sp = 0; sp < nst; ++sp) {
-        const bool live = 2 * sp + wg < nkb;
+      for (int sp = (int)((sa ^ step0) & 1); sp < nst; sp += 2) {
+        const int kb = 2 * sp + (wg & 1);
+        const bool live = kb < nkb;
         uint32_t out[32];
-        // this warpgroup's K block of the step, past the other's
-        for (int b = 0; b < 2 && ok; ++b) {
-          if (2 * sp + b >= nkb) break;
-          if (sub < 0) {
-            if (!warp_wait(bar.full_c + 8 * sc, phc, false)) { ok = false; break; }
-            sub = 0;
-          }
-          if (b == wg) {
-            uint32_t w[12];
-            const uint32_t cp = sbase + OFF_C + sc * C_BYTES + row * C_ROW + sub * 48;
+        if (live) {
+          // A row's codes are a stream of 16-byte chunks, eight to a line (stage): these are chunks 3 kb .. 3 kb + 2
+          const int l0 = 3 * kb >> 3, l1 = (3 * kb + 2) >> 3;
+          const uint32_t g0 = line0 + l0, g1 = line0 + l1;
+          const uint32_t s0 = g0 % SC, s1 = g1 % SC;
+          if (!warp_wait(bar.full_c + 8 * s0, (g0 / SC) & 1, false)) ok = false;
+          if (ok && l1 != l0 && !warp_wait(bar.full_c + 8 * s1, (g1 / SC) & 1, false)) ok = false;
+          if (!ok) break;
+          uint32_t w[12];
 #pragma unroll
-            for (int j = 0; j < 3; ++j) lds128(cp + 16 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            Lookup<64>::run(w, tbl, out);
+          for (int j = 0; j < 3; ++j) {
+            const int c = 3 * kb + j;
+            lds128(crow + ((c >> 3) == l0 ? s0 : s1) * C_BYTES + (((c ^ row) & 7) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2],
+                   w[4 * j + 3]);
           }
-          if (++sub == CKB || 2 * sp + b + 1 == nkb) {   // the stage's last K block
-            __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(bar.empty_c + 8 * sc);
-            sub = -1;
-            if (++sc == SC) {
-              sc = 0;
-              phc ^= 1;
-            }
+          Lookup<64>::run(w, tbl, out);
+          __syncwarp();
+          if (lane == 0) {
+            // a line is given back by its three or four K blocks; its last one arrives for those that it lacks
+            auto give = [&](int l, uint32_t s) {
+              const bool last = kb == min(nkb - 1, (8 * l + 7) / 3);
+              mbar_arrive_n(bar.empty_c + 8 * s, last ? 4 - (kb - 8 * l / 3) : 1);
+            };
+            give(l0, s0);
+            if (l1 != l0) give(l1, s1);
           }
         }
-        if (!ok) break;
-        if (!warp_wait(bar.empty_a + 8 * sa, pha, false)) { ok = false; break; }
+        if (!warp_wait(bar.empty_a + 8 * sa, (((step0 + sp) >> 1) & 1) ^ 1, false)) { ok = false; break; }
         if (live) {
           sm100::tc_fence_after();
-          sm100::tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + A_COL + sa * 64 + wg * 32, out);
+          sm100::tmem_st_32x32b_x32(to, out);
           sm100::tmem_wait_st();
           sm100::tc_fence_before();
           __syncwarp();
         }
-        if (lane == 0) sm100::mbar_arrive_cluster_relaxed(lead_ready + 8 * sa);
-        if (++sa == SA) {
-          sa = 0;
-          pha ^= 1;
-        }
+        if (lane == 0) sm100::mbar_arrive_cluster_relaxed(ready);
       }
       if (!ok) break;
       __syncwarp();
@@ -523,29 +554,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, es = (warp - 4) >> 2;   // this warp's lanes of tensor memory, and its slot
+    const int q = warp & 3;                    // this warp's lanes of tensor memory
     const uint32_t lead_empty = sm100::mapa_shared(bar.acc_empty, 0);
     Slots sl;
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
       const Tile t = tile_at(wi);
-      const bool runs = a.nseg > 1;            // both slots hold one tile's runs; its 16-column chunks alternate
+      const bool runs = a.nseg > 1;            // both slots hold one tile's runs
       const int slots = runs ? 2 : t.halves, first_slot = sl.take(slots), used0 = sl.used0, used1 = sl.used1;
       sl.done(first_slot, slots);
-      if (slots == 1 && es != first_slot) continue;
       const int n = GATED ? (t.wt * 2 + (int)rank) * (RW / 2) + 16 * q + (lane & 15)
                           : (t.wt * 2 + (int)rank) * RW + 32 * q + lane;
-      const int pbase = t.p0 + (t.halves == 2 ? es * t.nh : 0);
-      // the output row of position pbase + c + (lane & 15), -1 for none
-      auto row_of = [&](int c) {
-        const int p = pbase + c + (lane & 15);
-        if (c >= t.nh || p >= t.p1) return -1;
-        const int yr = a.g.y_rows ? __ldcg(a.g.y_rows + p) : p, xi = a.g.x_rows ? __ldcg(a.g.x_rows + p) : p;
-        return (unsigned)yr >= (unsigned)a.g.Y || xi < 0 || (a.g.x_rows ? xi / a.g.x_div : xi) >= a.g.X ? -1 : yr;
-      };
-      const int c0 = runs ? 16 * es : 0, step = runs ? 32 : 16;
-      int next = row_of(c0);
+      for (int h = 0; h < t.halves && ok; ++h) {
+      const int es = first_slot + h, pbase = t.p0 + h * t.nh;
+      // the output rows of the slot's positions, -1 for none: read while the products run
+      const uint32_t ylist = sbase + OFF_YROW + q * NS * 4;
+      __syncwarp();
+      for (int i = lane; i < t.nh; i += 32) {
+        const int p = pbase + i;
+        int yr = -1;
+        if (p < t.p1) {
+          const int xi = a.g.x_rows ? __ldcg(a.g.x_rows + p) : p;
+          yr = a.g.y_rows ? __ldcg(a.g.y_rows + p) : p;
+          if ((unsigned)yr >= (unsigned)a.g.Y || xi < 0 || (a.g.x_rows ? xi / a.g.x_div : xi) >= a.g.X) yr = -1;
+        }
+        sts32(ylist + 4 * i, (uint32_t)yr);
+      }
+      __syncwarp();
       if (!warp_wait(bar.acc_full + 8 * es, (es ? used1 : used0) & 1, true) ||
-          (runs && !warp_wait(bar.acc_full + 8 * (es ^ 1), (es ? used0 : used1) & 1, true))) {
+          (runs && !warp_wait(bar.acc_full + 8, used1 & 1, true))) {
         ok = false;
         break;
       }
@@ -565,28 +601,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         };
         const int mpos = GATED ? (lane & 7) + ((lane >> 4) << 3) : lane & 7, mf = GATED ? (lane >> 3) & 1 : lane >> 3;
         const int nb = (t.wt * 2 + (int)rank) * (GATED ? RW / 2 : RW) + FW * q;   // this warp's first feature
+        uint32_t lo[8], hi[8];                 // lanes 0-15 and 16-31 of this warp's quarter
+        sm100::tmem_ld_16x256b_x2(acc, lo);
+        sm100::tmem_ld_16x256b_x2(acc + (16u << 16), hi);
         for (int c = 0; c < t.nh; c += 16) {
-          uint32_t lo[8], hi[8];               // lanes 0-15 and 16-31 of this warp's quarter
-          sm100::tmem_ld_16x256b_x2(acc + c, lo);
-          sm100::tmem_ld_16x256b_x2(acc + c + (16u << 16), hi);
-          const int yr = next;
-          next = row_of(c + 16);
           sm100::tmem_wait_ld();
           if constexpr (GATED) {               // lo is g and hi is u of the same features and positions
 #pragma unroll
             for (int i = 0; i < 8; ++i) lo[i] = __float_as_uint(qld::silu_mul(__uint_as_float(lo[i]), __uint_as_float(hi[i])));
           }
-          auto two = [&](const uint32_t(&v)[8], int i) { return pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), OUT_BF16); };
+          uint32_t w[GATED ? 4 : 8];           // pairs of positions, round by round
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[GATED ? i : (i >> 1) * 4 + (i & 1)] = pack2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), OUT_BF16);
+            if constexpr (!GATED) w[(i >> 1) * 4 + 2 + (i & 1)] = pack2(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), OUT_BF16);
+          }
+          if (c + 16 < t.nh) {
+            sm100::tmem_ld_16x256b_x2(acc + c + 16, lo);
+            sm100::tmem_ld_16x256b_x2(acc + c + 16 + (16u << 16), hi);
+          }
+          __syncwarp();                        // the last chunk has been read out of the staging
+#pragma unroll
+          for (int r = 0; r < 16 / NP; ++r)
+            sm100::stmatrix_x4_trans(piece(NP * r + mpos, mf), w[4 * r], w[4 * r + 1], w[4 * r + 2], w[4 * r + 3]);
+          __syncwarp();
+          const int f8 = lane % PP;
 #pragma unroll
           for (int r = 0; r < 16 / NP; ++r) {
-            __syncwarp();                      // the last round has been read out of the staging
-            if constexpr (GATED)
-              sm100::stmatrix_x4_trans(piece(mpos, mf), two(lo, 0), two(lo, 2), two(lo, 4), two(lo, 6));
-            else
-              sm100::stmatrix_x4_trans(piece(mpos, mf), two(lo, 4 * r), two(lo, 4 * r + 2), two(hi, 4 * r), two(hi, 4 * r + 2));
-            __syncwarp();
-            const int pos = lane / PP, f8 = lane % PP;
-            const int yi = __shfl_sync(0xffffffffu, yr, NP * r + pos);
+            const int pos = NP * r + lane / PP, yi = (int)lds32(ylist + 4 * (c + pos));
             uint32_t x0, x1, x2, x3;
             lds128(piece(pos, f8), x0, x1, x2, x3);
             if (yi >= 0 && nb + 8 * f8 < a.N)
@@ -595,11 +637,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
       } else {
-      for (int c = c0; c < t.nh; c += step) {
+      for (int c = 0; c < t.nh; c += 16) {
         uint32_t v[16];
         sm100::tmem_ld_32x32b_x16(acc + c, v);
-        const int yr = next;
-        next = row_of(c + step);
         sm100::tmem_wait_ld();
         for (int r = 1; r < a.nseg; ++r) {
           uint32_t u[16];
@@ -616,13 +656,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const uint32_t mine = lane < 16 ? v[i] : v[8 + i], give = lane < 16 ? v[8 + i] : v[i];
             const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 16);
             const float gv = __uint_as_float(lane < 16 ? mine : got), uv = __uint_as_float(lane < 16 ? got : mine);
-            const int yi = __shfl_sync(0xffffffffu, yr, (lane < 16 ? 0 : 8) + i);
+            const int yi = (int)lds32(ylist + 4 * (c + (lane < 16 ? 0 : 8) + i));
             if (yi >= 0 && n < a.N) store_out(a.y, a.ydt, (size_t)yi * a.N + n, qld::silu_mul(gv, uv));
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int yi = __shfl_sync(0xffffffffu, yr, i);
+            const int yi = (int)lds32(ylist + 4 * (c + i));
             if (yi >= 0 && n < a.N) store_out(a.y, a.ydt, (size_t)yi * a.N + n, __uint_as_float(v[i]));
           }
         }
@@ -630,7 +670,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       sm100::tc_fence_before();
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive_cluster_relaxed(lead_empty + 8 * es);
+      if (lane == 0) {
+        sm100::mbar_arrive_cluster_relaxed(lead_empty + 8 * es);
+        if (runs) sm100::mbar_arrive_cluster_relaxed(lead_empty + 8);
+      }
+      }
     }
   }
 
@@ -686,10 +730,10 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
     const cuuint64_t rowbytes = (cuuint64_t)K * 3 / 4;
     const cuuint64_t dims[2] = {rowbytes, (cuuint64_t)g.G * N};
     const cuuint64_t strides[1] = {rowbytes};
-    const cuuint32_t box[2] = {C_ROW, (cuuint32_t)per};
+    const cuuint32_t box[2] = {C_LINE, (cuuint32_t)per};
     const cuuint32_t es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(c), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   CUtensorMap mc, mc2;

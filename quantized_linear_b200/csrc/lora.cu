@@ -1,102 +1,372 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   y_s[i] += scale_g B_{s,g} (A_{s,g} x[i]) for the rows i of adapter g, several layers of one x.
-// Two launches: t = A x (one warp per row, layer and rank index) into the workspace, then y += B t.
+//
+// Two launches over the plan's positions in tiles of one adapter each, so that an adapter's matrices are read
+// once per tile and not once per row:
+//   shrink  t = A x, tiles of 32 positions: the warps of a CTA (and up to KS CTAs) share out K; warp MMA with A's
+//           rows as M and the positions as N, so one position costs no more than eight;
+//   expand  y += B t, tiles of 64 positions by 256 features: t, summed over the K shares in order, scaled
+//           and split into a bf16 pair hi + lo (2^-17 relative), is the MMA's A from shared memory, B's rows its N.
+// Both are bound by memory: A and B of the adapters in use, and y read and written, which outweighs all else
+// when a tile is full.  The K index of a fragment is permuted (the same way on both sides), so that a lane's
+// elements are consecutive in memory: 16-byte loads of A and x, 8-byte loads of B.  The four 8-feature MMA
+// tiles of a strip interleave their features so that a lane ends with 8 consecutive ones of a row: 16-byte loads
+// and stores of a bf16 y.  Sums go in a fixed order: results do not depend on scheduling.
 #include <algorithm>
+#include <type_traits>
 
 #include "ql_internal.cuh"
 
 namespace {
 
 constexpr int MAX_LAYERS = 4;
+constexpr int ST = 32;               // positions per shrink tile
+constexpr int ET = 64;               // positions per expand tile
+constexpr int EF = 256;              // features per expand CTA: 8 warps x a strip of 32
+constexpr int KS_MAX = 8;            // CTAs that share K
+constexpr int WARPS = 8;
+constexpr unsigned FULL = 0xffffffffu;
 
 struct Layers {
   const uint16_t *A[MAX_LAYERS], *B[MAX_LAYERS];
   void *y[MAX_LAYERS];
   int N[MAX_LAYERS];
+  int chunk0[MAX_LAYERS + 1];        // expand: feature chunks before each layer
 };
 
-// the group of position p (offsets clamped to [0, T]), -1 for none
-__device__ __forceinline__ int group_at(const int32_t *offsets, int G, int p, int T) {
-  int lo = 0, hi = G;   // the last g with offsets[g] <= p
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (offsets[mid] <= p) lo = mid; else hi = mid - 1;
-  }
-  return lo < G && offsets[lo] <= p && p < offsets[lo + 1] ? lo : -1;
-}
-
-__global__ void __launch_bounds__(256)
-    lora_shrink_plain_kernel(const Layers L, int S, const uint16_t *x, const int32_t *order,
-                             const int32_t *offsets, const float *scale, int G, int T, int r,
-                             int K, float *t) {
+// The tile'th tile of `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
+__device__ __forceinline__ void find_tile(const int32_t *offsets, int G, int T, int tt, int tile, int &g, int &p0, int &p1) {
   const int lane = threadIdx.x & 31;
-  qld::pdl_trigger();
-  qld::pdl_wait();
-  const int64_t units = (int64_t)T * S * r;
-  for (int64_t u = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; u < units;
-       u += ((int64_t)gridDim.x * blockDim.x) >> 5) {
-    const int p = (int)(u / (S * r)), s = (int)(u / r % S), j = (int)(u % r);
-    const int g = group_at(offsets, G, p, T), row = order[p];
-    if (g < 0 || (unsigned)row >= (unsigned)T) continue;
-    const uint16_t *a = L.A[s] + ((int64_t)g * r + j) * K, *xr = x + (int64_t)row * K;
-    float acc = 0.f;
-    for (int k = lane; k < K; k += 32) acc = qld::fma_bf16(a[k], xr[k], acc);
+  g = -1;
+  int carry = 0;
+  for (int g0 = 0; g0 < G; g0 += 32) {
+    int a = 0, b = 0;
+    if (g0 + lane < G) {
+      a = max(0, min(T, __ldcg(offsets + g0 + lane)));
+      b = max(a, min(T, __ldcg(offsets + g0 + lane + 1)));
+    }
+    const int n = (b - a + tt - 1) / tt;
+    int s = n;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-    if (lane == 0) t[((int64_t)s * T + p) * r + j] = scale ? acc * scale[g] : acc;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(FULL, s, d);
+      if (lane >= d) s += u;
+    }
+    const bool mine = tile >= carry + s - n && tile < carry + s;
+    const unsigned who = __ballot_sync(FULL, mine);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      const int at = a + (tile - (carry + s - n)) * tt;
+      g = g0 + src;
+      p0 = __shfl_sync(FULL, at, src);
+      p1 = min(__shfl_sync(FULL, b, src), p0 + tt);
+      return;
+    }
+    carry += __shfl_sync(FULL, s, 31);
   }
 }
 
-__global__ void __launch_bounds__(256)
-    lora_expand_plain_kernel(const Layers L, int S, const int32_t *order, const int32_t *offsets,
-                             int ydt, int G, int T, int r, const float *t) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 bf16 from row[k .. k + 8), zeros from K on (or without a row)
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int K) {
+  if (row == nullptr || k >= K) return make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    return __ldcg(reinterpret_cast<const uint4 *>(row + k));
+  } else {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0;
+      v[i] = lo | (hi << 16);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// MT: 16-row tiles of A per pass.  Grid (tiles, layers, K shares).
+template <int MT, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32)
+    lora_shrink_kernel(const Layers L, const uint16_t *x, const int32_t *order, const int32_t *offsets, int G, int T,
+                       int r, int K, float *t) {
+  extern __shared__ __align__(16) float part[];   // [WARPS][MT * 16][ST + 1]
+  __shared__ int where[3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   qld::pdl_trigger();
   qld::pdl_wait();
-  for (int s = 0; s < S; ++s) {
-    const int N = L.N[s];
-    const int64_t units = (int64_t)T * N;
-    for (int64_t u = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; u < units; u += (int64_t)gridDim.x * blockDim.x) {
-      const int p = (int)(u / N), n = (int)(u - (int64_t)p * N);
-      const int g = group_at(offsets, G, p, T), row = order[p];
-      if (g < 0 || (unsigned)row >= (unsigned)T) continue;
-      const uint16_t *b = L.B[s] + ((int64_t)g * N + n) * r;
-      const float *tp = t + ((int64_t)s * T + p) * r;
-      float acc = 0.f;
-      for (int j = 0; j < r; ++j) acc = fmaf(qld::bf16_to_f32(b[j]), tp[j], acc);
-      if (ydt == QL_OUT_F32) {
-        static_cast<float *>(L.y[s])[(int64_t)row * N + n] += acc;
-      } else {
-        uint16_t *q = static_cast<uint16_t *>(L.y[s]) + (int64_t)row * N + n;
-        *q = qld::f32_to_bf16_rn(qld::bf16_to_f32(*q) + acc);
+  if (warp == 0) {
+    int g, p0 = 0, p1 = 0;
+    find_tile(offsets, G, T, ST, blockIdx.x, g, p0, p1);
+    if (lane == 0) where[0] = g, where[1] = p0, where[2] = p1;
+  }
+  __syncthreads();
+  const int g = where[0], p0 = where[1], p1 = where[2], s = blockIdx.y;
+  if (g < 0) return;
+  const int nt = (p1 - p0 + 7) / 8;               // 8-position tiles in use
+  const uint16_t *xr[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int p = p0 + 8 * n + gid, row = p < p1 ? __ldcg(order + p) : -1;
+    xr[n] = (unsigned)row < (unsigned)T ? x + (int64_t)row * K : nullptr;
+  }
+  // blocks of 32 inputs, shared out in order over CTAs, then warps
+  const int nb = (K + 31) / 32, shares = gridDim.z * WARPS, me = blockIdx.z * WARPS + warp;
+  const int b0 = (int)((int64_t)nb * me / shares), b1 = (int)((int64_t)nb * (me + 1) / shares);
+  for (int j0 = 0; j0 < r; j0 += 16 * MT) {
+    const uint16_t *ar[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = j0 + 16 * m + 8 * h + gid;
+        ar[m][h] = j < r ? L.A[s] + ((int64_t)g * r + j) * K : nullptr;
       }
+    float acc[MT][4][4] = {};
+#pragma unroll 2
+    for (int b = b0; b < b1; ++b) {
+      const int k = 32 * b + 8 * tig;
+      uint4 a[MT][2], v[4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[m][h] = load8<VEC>(ar[m][h], k, K);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (n < nt) v[n] = load8<VEC>(xr[n], k, K);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (n < nt) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma16816(acc[m][n], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, v[n].x, v[n].y);
+            mma16816(acc[m][n], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, v[n].z, v[n].w);
+          }
+        }
+    }
+    if (j0 > 0) __syncthreads();                  // the last pass's sums have been read
+    float *mine = part + warp * MT * 16 * (ST + 1);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (n < nt) {
+          float *d = mine + (16 * m + gid) * (ST + 1) + 8 * n + 2 * tig;
+          d[0] = acc[m][n][0];
+          d[1] = acc[m][n][1];
+          d[8 * (ST + 1)] = acc[m][n][2];
+          d[8 * (ST + 1) + 1] = acc[m][n][3];
+        }
+    __syncthreads();
+    const int ranks = min(16 * MT, r - j0);
+    float *out = t + (((int64_t)blockIdx.z * gridDim.y + s) * T + p0) * r + j0;
+    for (int i = threadIdx.x; i < ranks * (p1 - p0); i += WARPS * 32) {
+      const int p = i / ranks, j = i - p * ranks;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += part[(w * MT * 16 + j) * (ST + 1) + p];
+      out[(int64_t)p * r + j] = sum;
     }
   }
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr));
+}
+
+// 4 bf16 of a row of B from k on: k .. k + 3, zeros from r on
+__device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int r, bool vec) {
+  if (row == nullptr || k >= r) return make_uint2(0, 0);
+  if (vec) return __ldg(reinterpret_cast<const uint2 *>(row + k));
+  const uint32_t e0 = row[k], e1 = k + 1 < r ? row[k + 1] : 0, e2 = k + 2 < r ? row[k + 2] : 0, e3 = k + 3 < r ? row[k + 3] : 0;
+  return make_uint2(e0 | (e1 << 16), e2 | (e3 << 16));
+}
+
+// Grid (feature chunks of all layers, tiles).
+template <bool F32>
+__global__ void __launch_bounds__(WARPS * 32, 2)
+    lora_expand_kernel(const Layers L, int S, const int32_t *order, const int32_t *offsets, const float *scale, int G,
+                       int T, int r, int shares, const float *t) {
+  extern __shared__ __align__(16) unsigned char esm[];   // t as bf16: [hi, lo][ET][rp], rows of rp * 2 bytes
+  __shared__ int where[3], rows[ET];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int r16 = (r + 15) / 16, rp = r16 * 16 + 8;      // an odd number of 16-byte pieces: no bank conflicts
+  qld::pdl_trigger();
+  qld::pdl_wait();
+  if (warp == 0) {
+    int g, p0 = 0, p1 = 0;
+    find_tile(offsets, G, T, ET, blockIdx.y, g, p0, p1);
+    if (lane == 0) where[0] = g, where[1] = p0, where[2] = p1;
+  }
+  __syncthreads();
+  const int g = where[0], p0 = where[1], count = where[2] - p0;
+  if (g < 0) return;
+  int s = 0;
+  while (s + 1 < S && (int)blockIdx.x >= L.chunk0[s + 1]) ++s;
+  const int N = L.N[s], n0 = ((int)blockIdx.x - L.chunk0[s]) * EF + 32 * warp;
+  const int mt = (count + 15) / 16;
+  if (threadIdx.x < ET) {
+    const int row = (int)threadIdx.x < count ? __ldcg(order + p0 + threadIdx.x) : -1;
+    rows[threadIdx.x] = (unsigned)row < (unsigned)T ? row : -1;
+  }
+  uint16_t *hi = reinterpret_cast<uint16_t *>(esm), *lo = hi + ET * rp;
+  const float f = scale ? __ldcg(scale + g) : 1.f;
+  for (int i = threadIdx.x; i < mt * 16 * r16 * 16; i += WARPS * 32) {
+    const int p = i / (r16 * 16), j = i - p * (r16 * 16);
+    float v = 0.f;
+    if (p < count && j < r) {
+      const float *src = t + ((int64_t)s * T + p0 + p) * r + j;
+      for (int z = 0; z < shares; ++z) v += __ldcg(src + (int64_t)z * S * T * r);
+      v *= f;
+    }
+    const uint16_t h = qld::f32_to_bf16_rn(v);
+    const float rest = v - qld::bf16_to_f32(h);
+    // place of rank index j within its 16: lane (j % 16) / 4 takes elements j % 4 as fragment columns 2 tig, 2 tig + 8
+    const int e = j & 3, at = (j & ~15) + 2 * ((j & 15) >> 2) + (e & 1) + 8 * (e >> 1);
+    hi[p * rp + at] = h;
+    lo[p * rp + at] = (rest == rest) ? qld::f32_to_bf16_rn(rest) : 0;   // inf and NaN are in hi alone
+  }
+  __syncthreads();
+  if (n0 >= N) return;
+  // MMA column c of the strip's tile i is feature n0 + 8 (c / 2) + 2 i + c % 2
+  const uint16_t *br[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + 8 * (gid >> 1) + 2 * i + (gid & 1);
+    br[i] = n < N ? L.B[s] + ((int64_t)g * N + n) * r : nullptr;
+  }
+  const bool vec = r % 4 == 0;
+  const uint32_t frag = static_cast<uint32_t>(__cvta_generic_to_shared(hi)) + ((lane & 15) * rp + (lane >> 4) * 8) * 2;
+  float acc[4][4][4] = {};
+  for (int k = 0; k < r16; ++k) {
+    uint2 b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = load4(br[i], 16 * k + 4 * tig, r, vec);
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      if (m < mt) {
+        uint32_t ah[4], al[4];
+        ldmatrix_x4(frag + (16 * m * rp + 16 * k) * 2, ah);
+        ldmatrix_x4(frag + ((ET + 16 * m) * rp + 16 * k) * 2, al);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mma16816(acc[m][i], al[0], al[1], al[2], al[3], b[i].x, b[i].y);
+          mma16816(acc[m][i], ah[0], ah[1], ah[2], ah[3], b[i].x, b[i].y);
+        }
+      }
+  }
+  // this lane's features n .. n + 7 of positions gid and gid + 8 of each 16
+  const int n = n0 + 8 * tig;
+  const bool whole = N % 8 == 0;                  // 16-byte aligned pieces, none partial
+  if (n >= N) return;
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+    if (m < mt) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = rows[16 * m + 8 * h + gid];
+        if (row < 0) continue;
+        const size_t o = (size_t)row * N + n;
+        float add[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          add[2 * i] = acc[m][i][2 * h];
+          add[2 * i + 1] = acc[m][i][2 * h + 1];
+        }
+        if constexpr (F32) {
+          float *y = static_cast<float *>(L.y[s]) + o;
+          if (whole) {
+            float4 *v = reinterpret_cast<float4 *>(y);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float4 w = __ldcg(v + i);
+              w.x += add[4 * i]; w.y += add[4 * i + 1]; w.z += add[4 * i + 2]; w.w += add[4 * i + 3];
+              v[i] = w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (n + i < N) y[i] += add[i];
+          }
+        } else {
+          uint16_t *y = static_cast<uint16_t *>(L.y[s]) + o;
+          if (whole) {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(y));
+            uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              u[i] = uint32_t(qld::f32_to_bf16_rn(qld::bf16_to_f32(u[i] & 0xffffu) + add[2 * i])) |
+                     (uint32_t(qld::f32_to_bf16_rn(__uint_as_float(u[i] & 0xffff0000u) + add[2 * i + 1])) << 16);
+            *reinterpret_cast<uint4 *>(y) = make_uint4(u[0], u[1], u[2], u[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (n + i < N) y[i] = qld::f32_to_bf16_rn(qld::bf16_to_f32(y[i]) + add[i]);
+          }
+        }
+      }
+    }
+}
+
+// CTAs that share K: enough that the shrink tiles of an ordinary batch fill the SMs, each with at least four blocks of
+// 32 inputs per warp.  (Depends on the call's sizes alone, so that results do.)
+int k_shares(int S, int G, int T, int K) {
+  const int64_t tiles = ((int64_t)std::min(G, T) + T / ST) * S;
+  const int64_t want = std::max<int64_t>(1, 2 * 148 / std::max<int64_t>(1, tiles));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, KS_MAX, K / (32 * WARPS * 4)}));
 }
 
 }  // namespace
 
 namespace ql {
 
-size_t lora_workspace_size(int S, int T, int r) { return ((size_t)S * T * r * sizeof(float) + 255) / 256 * 256; }
+size_t lora_workspace_size(int S, int T, int r) { return ((size_t)KS_MAX * S * T * r * sizeof(float) + 255) / 256 * 256; }
 
 ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order,
                           const int32_t *offsets, const float *scale, ql_out_dtype ydt, int G, int T, int r, int K,
                           void *ws, cudaStream_t s) {
   Layers L{};
-  int64_t cols = 0;
   for (int i = 0; i < S; ++i) {
     L.A[i] = layers[i].A;
     L.B[i] = layers[i].B;
     L.y[i] = layers[i].y;
     L.N[i] = layers[i].N;
-    cols = std::max<int64_t>(cols, layers[i].N);
+    L.chunk0[i + 1] = L.chunk0[i] + (layers[i].N + EF - 1) / EF;
   }
   float *t = static_cast<float *>(ws);
-  const int64_t most = (int64_t)sm_count() * 8;
-  launch(lora_shrink_plain_kernel, (int)std::min<int64_t>(((int64_t)T * S * r + 7) / 8, most), 256, 0, s, L, S, x, order,
-         offsets, scale, G, T, r, K, t);
-  launch(lora_expand_plain_kernel, (int)std::min<int64_t>((T * cols + 255) / 256, most), 256, 0, s, L, S, order, offsets,
-         (int)ydt, G, T, r, t);
+  const int shares = k_shares(S, G, T, K);
+  auto tiles = [&](int tt) { return (unsigned)(std::min(G, T) + T / tt); };   // the most that the counts could make
+  auto shrink = [&](auto mtc, auto vecc) -> bool {
+    constexpr int MT = decltype(mtc)::value;
+    auto kern = lora_shrink_kernel<MT, decltype(vecc)::value>;
+    const size_t smem = (size_t)WARPS * MT * 16 * (ST + 1) * sizeof(float);
+    if (smem > 48 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
+    launch(kern, dim3(tiles(ST), S, shares), WARPS * 32, smem, s, L, x, order, offsets, G, T, r, K, t);
+    return true;
+  };
+  auto by_rank = [&](auto vecc) {
+    return r <= 16 ? shrink(std::integral_constant<int, 1>{}, vecc)
+           : r <= 32 ? shrink(std::integral_constant<int, 2>{}, vecc)
+                     : shrink(std::integral_constant<int, 4>{}, vecc);
+  };
+  if (!(K % 8 == 0 ? by_rank(std::true_type{}) : by_rank(std::false_type{})))
+    return fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
+  const size_t smem = (size_t)2 * ET * ((r + 15) / 16 * 16 + 8) * 2;
+  auto expand = [&](auto kern) -> bool {
+    if (smem > 48 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
+    launch(kern, dim3(L.chunk0[S], tiles(ET)), WARPS * 32, smem, s, L, S, order, offsets, scale, G, T, r, shares,
+           static_cast<const float *>(t));
+    return true;
+  };
+  if (!(ydt == QL_OUT_F32 ? expand(lora_expand_kernel<true>) : expand(lora_expand_kernel<false>)))
+    return fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
   return launch_status("lora_add");
 }
 

@@ -246,7 +246,7 @@ void launch_route(const void *logits, ql_out_dtype ldt, int T, int E, int k, int
                   float *weights, int *hist, int32_t *order, int32_t *offsets, cudaStream_t s) {
   if (T <= ONE_TOKENS) {
     const size_t smem = scatter_smem(32, E);
-    if (smem > 48 * 1024) (void)ql::set_max_smem(moe_route_kernel<V, true>, (int)smem);
+    if (smem > 40 * 1024) (void)ql::set_max_smem(moe_route_kernel<V, true>, (int)smem);
     ql::launch(moe_route_kernel<V, true>, 1, 1024, smem, s, logits, (int)ldt, T, E, k, normalize, T, experts, weights,
                hist, order, offsets);
   } else {
@@ -261,7 +261,7 @@ void launch_place(const int32_t *index, int M, int G, Chunks c, const int *hist,
                   cudaStream_t s) {
   const int threads = hist ? 256 : 1024;
   const size_t smem = scatter_smem(threads / 32, G);
-  if (smem > 48 * 1024) (void)ql::set_max_smem(group_place_kernel, (int)smem);
+  if (smem > 40 * 1024) (void)ql::set_max_smem(group_place_kernel, (int)smem);
   ql::launch(group_place_kernel, std::max(1, c.count), threads, smem, s, index, M, G, c.size, hist, c.count, order,
              offsets);
 }

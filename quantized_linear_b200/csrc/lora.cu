@@ -3,10 +3,12 @@
 //
 // Two launches over the plan's positions in tiles of one adapter each, so that an adapter's matrices are read
 // once per tile and not once per row:
-//   shrink  t = A x, tiles of 32 positions: the warps of a CTA (and up to KS CTAs) share out K; warp MMA with A's
-//           rows as M and the positions as N, so one position costs no more than eight;
-//   expand  y += B t, tiles of 64 positions by 256 features: t, summed over the K shares in order, scaled
-//           and split into a bf16 pair hi + lo (2^-17 relative), is the MMA's A from shared memory, B's rows its N.
+//   shrink  t = A x: A's rows are the warp MMA's M and the positions its N, so one position costs no more than
+//           eight; the warps of a CTA and up to KS_MAX CTAs share out K.  Few rows per adapter: tiles of 32 positions,
+//           fragments loaded straight from memory.  Many: tiles of 64, through a ring of asynchronous copies;
+//   expand  y += B t, tiles of 16 to 64 positions by strips of 32 features per warp: t, summed over the K shares in
+//           order, scaled and split into a bf16 pair hi + lo (2^-17 relative), is the MMA's A from shared memory,
+//           B's rows its N.
 // Both are bound by memory: A and B of the adapters in use, and y read and written, which outweighs all else
 // when a tile is full.  The K index of a fragment is permuted (the same way on both sides), so that a lane's
 // elements are consecutive in memory: 16-byte loads of A and x, 8-byte loads of B.  The four 8-feature MMA
@@ -21,8 +23,10 @@ namespace {
 
 constexpr int MAX_LAYERS = 4;
 constexpr int ST = 32;               // positions per shrink tile
-constexpr int ET = 64;               // positions per expand tile
-constexpr int EF = 256;              // features per expand CTA: 8 warps x a strip of 32
+constexpr int RT = 64;               // positions per shrink tile of the ring form
+constexpr int RK = 64;               // inputs per stage of its ring
+constexpr int RSTAGES = 4;
+constexpr int EF = 256;              // features per round of an expand CTA: 8 warps x a strip of 32
 constexpr int KS_MAX = 8;            // CTAs that share K
 constexpr int WARPS = 8;
 constexpr unsigned FULL = 0xffffffffu;
@@ -31,7 +35,7 @@ struct Layers {
   const uint16_t *A[MAX_LAYERS], *B[MAX_LAYERS];
   void *y[MAX_LAYERS];
   int N[MAX_LAYERS];
-  int chunk0[MAX_LAYERS + 1];        // expand: feature chunks before each layer
+  int chunk0[MAX_LAYERS + 1];        // expand: CTAs (runs of feature rounds) before each layer
 };
 
 // The tile'th tile of `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
@@ -181,6 +185,119 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&v)[4]) {
                : "r"(addr));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// The ring form (K % 8 == 0): 64 positions x MT * 16 ranks.  A stage is 64 inputs of the tile's x rows and of the
+// adapter's A rows, 128-byte rows whose 16-byte pieces are permuted by the row (ldmatrix reads eight rows without a
+// bank conflict).  Warp w multiplies inputs 16 (w % 4) .. + 15 of each stage for positions 32 (w / 4) .. + 31, so every
+// fragment is loaded once; the four warps' sums meet in shared memory at the end.
+template <int MT>
+__global__ void __launch_bounds__(WARPS * 32, 2)
+    lora_shrink_ring_kernel(const Layers L, const uint16_t *x, const int32_t *order, const int32_t *offsets, int G, int T,
+                            int r, int K, float *t) {
+  constexpr int ROWS = RT + 16 * MT, STAGE = ROWS * 128;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ int where[3];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  qld::pdl_trigger();
+  qld::pdl_wait();
+  if (warp == 0) {
+    int g, p0 = 0, p1 = 0;
+    find_tile(offsets, G, T, RT, blockIdx.x, g, p0, p1);
+    if (lane == 0) where[0] = g, where[1] = p0, where[2] = p1;
+  }
+  __syncthreads();
+  const int g = where[0], p0 = where[1], count = where[2] - p0, s = blockIdx.y;
+  if (g < 0) return;
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  const int ns = (K + RK - 1) / RK;
+  const int s0 = (int)((int64_t)ns * blockIdx.z / gridDim.z), s1 = (int)((int64_t)ns * (blockIdx.z + 1) / gridDim.z);
+  const int ch = threadIdx.x & 7, r0 = threadIdx.x >> 3;      // this thread's 16-byte piece, and its rows r0 + 32 i
+  constexpr int PER = (ROWS + 31) / 32;
+  for (int j0 = 0; j0 < r; j0 += 16 * MT) {
+    const uint16_t *src[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int row = r0 + 32 * i;
+      src[i] = nullptr;
+      if (row < RT) {
+        const int at = row < count ? __ldcg(order + p0 + row) : -1;
+        if ((unsigned)at < (unsigned)T) src[i] = x + (int64_t)at * K;
+      } else if (row < ROWS && j0 + row - RT < r) {
+        src[i] = L.A[s] + ((int64_t)g * r + j0 + row - RT) * K;
+      }
+    }
+    auto fetch = [&](int st) {
+      if (st < s1) {
+        const uint32_t to = sb + ((st - s0) % RSTAGES) * STAGE;
+        const int k = st * RK + 8 * ch;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int row = r0 + 32 * i;
+          const bool there = src[i] != nullptr && k < K;
+          if (row < ROWS) cp_async16(to + row * 128 + ((ch ^ (row & 7)) << 4), there ? src[i] + k : x, there);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncthreads();                              // the last pass's sums have been read
+#pragma unroll
+    for (int st = 0; st < RSTAGES - 1; ++st) fetch(s0 + st);
+    const int kq = warp & 3, half = warp >> 2;
+    const int nt = max(0, min(4, (count - 32 * half + 7) / 8));
+    float acc[MT][4][4] = {};
+    for (int st = s0; st < s1; ++st) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(RSTAGES - 2) : "memory");
+      __syncthreads();
+      fetch(st + RSTAGES - 1);
+      const uint32_t at = sb + ((st - s0) % RSTAGES) * STAGE;
+      // x: matrices (positions 0-7, inputs 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15); A: (ranks 0-7, inputs 0-7),
+      // (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+      uint32_t v[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int row = 32 * half + 16 * n + (lane & 7) + ((lane >> 4) << 3), piece = 2 * kq + ((lane >> 3) & 1);
+        if (2 * n < nt) ldmatrix_x4(at + row * 128 + ((piece ^ (row & 7)) << 4), v[n]);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t a[4];
+        const int row = RT + 16 * m + (lane & 15), piece = 2 * kq + (lane >> 4);
+        ldmatrix_x4(at + row * 128 + ((piece ^ (row & 7)) << 4), a);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (n < nt) mma16816(acc[m][n], a[0], a[1], a[2], a[3], v[n >> 1][2 * (n & 1)], v[n >> 1][2 * (n & 1) + 1]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float *part = reinterpret_cast<float *>(ring);             // [4][RT][MT * 16 + 4]
+    constexpr int LD = MT * 16 + 4;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (n < nt) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          float *d = part + (kq * RT + 32 * half + 8 * n + 2 * tig) * LD + 16 * m + gid;
+          d[0] = acc[m][n][0];
+          d[LD] = acc[m][n][1];
+          d[8] = acc[m][n][2];
+          d[LD + 8] = acc[m][n][3];
+        }
+      }
+    __syncthreads();
+    const int ranks = min(16 * MT, r - j0);
+    float *out = t + (((int64_t)blockIdx.z * gridDim.y + s) * T + p0) * r + j0;
+    for (int i = threadIdx.x; i < ranks * count; i += WARPS * 32) {
+      const int p = i / ranks, j = i - p * ranks;
+      const float *d = part + p * LD + j;
+      out[(int64_t)p * r + j] = d[0] + d[RT * LD] + d[2 * RT * LD] + d[3 * RT * LD];
+    }
+  }
+}
+
 // 4 bf16 of a row of B from k on: k .. k + 3, zeros from r on
 __device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int r, bool vec) {
   if (row == nullptr || k >= r) return make_uint2(0, 0);
@@ -189,11 +306,13 @@ __device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int r, bool v
   return make_uint2(e0 | (e1 << 16), e2 | (e3 << 16));
 }
 
-// Grid (feature chunks of all layers, tiles).
-template <bool F32>
-__global__ void __launch_bounds__(WARPS * 32, 2)
+// Tiles of 16 MTL positions; grid (runs of `rounds` feature rounds of all layers, tiles).  The y values of a strip are
+// requested before its products, so that the two overlap.
+template <bool F32, int MTL>
+__global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 4 : 2)
     lora_expand_kernel(const Layers L, int S, const int32_t *order, const int32_t *offsets, const float *scale, int G,
-                       int T, int r, int shares, const float *t) {
+                       int T, int r, int shares, int rounds, const float *t) {
+  constexpr int ET = 16 * MTL;
   extern __shared__ __align__(16) unsigned char esm[];   // t as bf16: [hi, lo][ET][rp], rows of rp * 2 bytes
   __shared__ int where[3], rows[ET];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -204,18 +323,20 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     int g, p0 = 0, p1 = 0;
     find_tile(offsets, G, T, ET, blockIdx.y, g, p0, p1);
     if (lane == 0) where[0] = g, where[1] = p0, where[2] = p1;
+    if (g >= 0) {
+      for (int i = lane; i < ET; i += 32) {
+        const int row = p0 + i < p1 ? __ldcg(order + p0 + i) : -1;
+        rows[i] = (unsigned)row < (unsigned)T ? row : -1;
+      }
+    }
   }
   __syncthreads();
   const int g = where[0], p0 = where[1], count = where[2] - p0;
   if (g < 0) return;
   int s = 0;
   while (s + 1 < S && (int)blockIdx.x >= L.chunk0[s + 1]) ++s;
-  const int N = L.N[s], n0 = ((int)blockIdx.x - L.chunk0[s]) * EF + 32 * warp;
-  const int mt = (count + 15) / 16;
-  if (threadIdx.x < ET) {
-    const int row = (int)threadIdx.x < count ? __ldcg(order + p0 + threadIdx.x) : -1;
-    rows[threadIdx.x] = (unsigned)row < (unsigned)T ? row : -1;
-  }
+  const int N = L.N[s], f0 = ((int)blockIdx.x - L.chunk0[s]) * rounds * EF + 32 * warp;
+  const int mt = MTL == 1 ? 1 : (count + 15) / 16;
   uint16_t *hi = reinterpret_cast<uint16_t *>(esm), *lo = hi + ET * rp;
   const float f = scale ? __ldcg(scale + g) : 1.f;
   for (int i = threadIdx.x; i < mt * 16 * r16 * 16; i += WARPS * 32) {
@@ -223,6 +344,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     float v = 0.f;
     if (p < count && j < r) {
       const float *src = t + ((int64_t)s * T + p0 + p) * r + j;
+#pragma unroll 4
       for (int z = 0; z < shares; ++z) v += __ldcg(src + (int64_t)z * S * T * r);
       v *= f;
     }
@@ -234,46 +356,59 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
     lo[p * rp + at] = (rest == rest) ? qld::f32_to_bf16_rn(rest) : 0;   // inf and NaN are in hi alone
   }
   __syncthreads();
-  if (n0 >= N) return;
-  // MMA column c of the strip's tile i is feature n0 + 8 (c / 2) + 2 i + c % 2
-  const uint16_t *br[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = n0 + 8 * (gid >> 1) + 2 * i + (gid & 1);
-    br[i] = n < N ? L.B[s] + ((int64_t)g * N + n) * r : nullptr;
-  }
-  const bool vec = r % 4 == 0;
+  const bool vec = r % 4 == 0;                    // 8-byte aligned rows of B
+  const bool whole = N % 8 == 0;                  // 16-byte aligned pieces of y, none partial
   const uint32_t frag = static_cast<uint32_t>(__cvta_generic_to_shared(hi)) + ((lane & 15) * rp + (lane >> 4) * 8) * 2;
-  float acc[4][4][4] = {};
-  for (int k = 0; k < r16; ++k) {
-    uint2 b[4];
+  for (int rd = 0; rd < rounds; ++rd) {
+    const int n0 = f0 + rd * EF;
+    if (n0 >= N) return;
+    const int n = n0 + 8 * tig;                   // this lane's features n .. n + 7, of positions gid and gid + 8 of each 16
+    uint4 old[MTL][2][F32 ? 2 : 1];
+    if (whole && n < N) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = load4(br[i], 16 * k + 4 * tig, r, vec);
+      for (int m = 0; m < MTL; ++m)
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-      if (m < mt) {
-        uint32_t ah[4], al[4];
-        ldmatrix_x4(frag + (16 * m * rp + 16 * k) * 2, ah);
-        ldmatrix_x4(frag + ((ET + 16 * m) * rp + 16 * k) * 2, al);
+        for (int h = 0; h < 2; ++h) {
+          const int row = rows[16 * m + 8 * h + gid];
+          if (row < 0) continue;
+          const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const char *>(L.y[s]) + ((size_t)row * N + n) * (F32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma16816(acc[m][i], al[0], al[1], al[2], al[3], b[i].x, b[i].y);
-          mma16816(acc[m][i], ah[0], ah[1], ah[2], ah[3], b[i].x, b[i].y);
+          for (int i = 0; i < (F32 ? 2 : 1); ++i) old[m][h][i] = __ldcg(v + i);
         }
-      }
-  }
-  // this lane's features n .. n + 7 of positions gid and gid + 8 of each 16
-  const int n = n0 + 8 * tig;
-  const bool whole = N % 8 == 0;                  // 16-byte aligned pieces, none partial
-  if (n >= N) return;
+    }
+    // MMA column c of the strip's tile i is feature n0 + 8 (c / 2) + 2 i + c % 2
+    const uint16_t *br[4];
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
-    if (m < mt) {
+    for (int i = 0; i < 4; ++i) {
+      const int c = n0 + 8 * (gid >> 1) + 2 * i + (gid & 1);
+      br[i] = c < N ? L.B[s] + ((int64_t)g * N + c) * r : nullptr;
+    }
+    float acc[MTL][4][4] = {};
+#pragma unroll 2
+    for (int k = 0; k < r16; ++k) {
+      uint2 b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = load4(br[i], 16 * k + 4 * tig, r, vec);
+#pragma unroll
+      for (int m = 0; m < MTL; ++m)
+        if (m < mt) {
+          uint32_t ah[4], al[4];
+          ldmatrix_x4(frag + (16 * m * rp + 16 * k) * 2, ah);
+          ldmatrix_x4(frag + ((ET + 16 * m) * rp + 16 * k) * 2, al);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mma16816(acc[m][i], al[0], al[1], al[2], al[3], b[i].x, b[i].y);
+            mma16816(acc[m][i], ah[0], ah[1], ah[2], ah[3], b[i].x, b[i].y);
+          }
+        }
+    }
+    if (n >= N) continue;
+#pragma unroll
+    for (int m = 0; m < MTL; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = rows[16 * m + 8 * h + gid];
         if (row < 0) continue;
-        const size_t o = (size_t)row * N + n;
         float add[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -281,14 +416,14 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
           add[2 * i + 1] = acc[m][i][2 * h + 1];
         }
         if constexpr (F32) {
-          float *y = static_cast<float *>(L.y[s]) + o;
+          float *y = static_cast<float *>(L.y[s]) + (size_t)row * N + n;
           if (whole) {
-            float4 *v = reinterpret_cast<float4 *>(y);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float4 w = __ldcg(v + i);
-              w.x += add[4 * i]; w.y += add[4 * i + 1]; w.z += add[4 * i + 2]; w.w += add[4 * i + 3];
-              v[i] = w;
+              const uint4 w = old[m][h][i];
+              reinterpret_cast<float4 *>(y)[i] =
+                  make_float4(__uint_as_float(w.x) + add[4 * i], __uint_as_float(w.y) + add[4 * i + 1],
+                              __uint_as_float(w.z) + add[4 * i + 2], __uint_as_float(w.w) + add[4 * i + 3]);
             }
           } else {
 #pragma unroll
@@ -296,10 +431,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
               if (n + i < N) y[i] += add[i];
           }
         } else {
-          uint16_t *y = static_cast<uint16_t *>(L.y[s]) + o;
+          uint16_t *y = static_cast<uint16_t *>(L.y[s]) + (size_t)row * N + n;
           if (whole) {
-            const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(y));
-            uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            uint32_t u[4] = {old[m][h][0].x, old[m][h][0].y, old[m][h][0].z, old[m][h][0].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               u[i] = uint32_t(qld::f32_to_bf16_rn(qld::bf16_to_f32(u[i] & 0xffffu) + add[2 * i])) |
@@ -312,15 +446,19 @@ __global__ void __launch_bounds__(WARPS * 32, 2)
           }
         }
       }
-    }
+  }
 }
 
-// CTAs that share K: enough that the shrink tiles of an ordinary batch fill the SMs, each with at least four blocks of
-// 32 inputs per warp.  (Depends on the call's sizes alone, so that results do.)
+// Whether the tiles of 64 positions fill: 16 rows per adapter on average, or more.
+bool many_rows(int G, int T) { return T / std::min(G, T) >= 16; }
+
+// CTAs that share K: enough that the shrink tiles of an ordinary batch fill the SMs, each with a few blocks of inputs per
+// warp.  (Depends on the call's sizes alone, so that results do.)
 int k_shares(int S, int G, int T, int K) {
-  const int64_t tiles = ((int64_t)std::min(G, T) + T / ST) * S;
+  const bool ring = many_rows(G, T) && K % 8 == 0;
+  const int64_t tiles = ((int64_t)std::min(G, T) + T / (ring ? RT : ST)) * S;
   const int64_t want = std::max<int64_t>(1, 2 * 148 / std::max<int64_t>(1, tiles));
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, KS_MAX, K / (32 * WARPS * 4)}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, KS_MAX, K / (ring ? RK * 8 : 32 * WARPS * 4)}));
 }
 
 }  // namespace
@@ -332,40 +470,49 @@ size_t lora_workspace_size(int S, int T, int r) { return ((size_t)KS_MAX * S * T
 ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order,
                           const int32_t *offsets, const float *scale, ql_out_dtype ydt, int G, int T, int r, int K,
                           void *ws, cudaStream_t s) {
+  const bool many = many_rows(G, T), ring = many && K % 8 == 0;
+  // feature rounds per expand CTA: t is prepared once for them; few tiles need the CTAs
+  const int rounds = many && T >= 1024 ? 4 : 1;
   Layers L{};
   for (int i = 0; i < S; ++i) {
     L.A[i] = layers[i].A;
     L.B[i] = layers[i].B;
     L.y[i] = layers[i].y;
     L.N[i] = layers[i].N;
-    L.chunk0[i + 1] = L.chunk0[i] + (layers[i].N + EF - 1) / EF;
+    L.chunk0[i + 1] = L.chunk0[i] + (layers[i].N + EF * rounds - 1) / (EF * rounds);
   }
   float *t = static_cast<float *>(ws);
   const int shares = k_shares(S, G, T, K);
   auto tiles = [&](int tt) { return (unsigned)(std::min(G, T) + T / tt); };   // the most that the counts could make
-  auto shrink = [&](auto mtc, auto vecc) -> bool {
-    constexpr int MT = decltype(mtc)::value;
-    auto kern = lora_shrink_kernel<MT, decltype(vecc)::value>;
-    const size_t smem = (size_t)WARPS * MT * 16 * (ST + 1) * sizeof(float);
-    if (smem > 48 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
-    launch(kern, dim3(tiles(ST), S, shares), WARPS * 32, smem, s, L, x, order, offsets, G, T, r, K, t);
+  auto shrink = [&](auto kern, int tile, size_t smem) -> bool {
+    if (smem > 40 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
+    launch(kern, dim3(tiles(tile), S, shares), WARPS * 32, smem, s, L, x, order, offsets, G, T, r, K, t);
     return true;
   };
-  auto by_rank = [&](auto vecc) {
-    return r <= 16 ? shrink(std::integral_constant<int, 1>{}, vecc)
-           : r <= 32 ? shrink(std::integral_constant<int, 2>{}, vecc)
-                     : shrink(std::integral_constant<int, 4>{}, vecc);
+  auto by_rank = [&](auto mtc) {
+    constexpr int MT = decltype(mtc)::value;
+    constexpr size_t part = (size_t)WARPS * MT * 16 * (ST + 1) * sizeof(float);
+    constexpr size_t rsum = (size_t)4 * RT * (MT * 16 + 4) * sizeof(float), rbuf = (size_t)RSTAGES * (RT + 16 * MT) * 128;
+    if (ring) return shrink(lora_shrink_ring_kernel<MT>, RT, std::max(rsum, rbuf));
+    return K % 8 == 0 ? shrink(lora_shrink_kernel<MT, true>, ST, part) : shrink(lora_shrink_kernel<MT, false>, ST, part);
   };
-  if (!(K % 8 == 0 ? by_rank(std::true_type{}) : by_rank(std::false_type{})))
+  if (!(r <= 16   ? by_rank(std::integral_constant<int, 1>{})
+        : r <= 32 ? by_rank(std::integral_constant<int, 2>{})
+                  : by_rank(std::integral_constant<int, 4>{})))
     return fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
-  const size_t smem = (size_t)2 * ET * ((r + 15) / 16 * 16 + 8) * 2;
-  auto expand = [&](auto kern) -> bool {
-    if (smem > 48 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
-    launch(kern, dim3(L.chunk0[S], tiles(ET)), WARPS * 32, smem, s, L, S, order, offsets, scale, G, T, r, shares,
+  auto expand = [&](auto f32c, auto mtl) -> bool {
+    constexpr int ET = 16 * decltype(mtl)::value;
+    auto kern = lora_expand_kernel<decltype(f32c)::value, decltype(mtl)::value>;
+    const size_t smem = (size_t)2 * ET * ((r + 15) / 16 * 16 + 8) * 2;
+    if (smem > 40 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
+    launch(kern, dim3(L.chunk0[S], tiles(ET)), WARPS * 32, smem, s, L, S, order, offsets, scale, G, T, r, shares, rounds,
            static_cast<const float *>(t));
     return true;
   };
-  if (!(ydt == QL_OUT_F32 ? expand(lora_expand_kernel<true>) : expand(lora_expand_kernel<false>)))
+  using One = std::integral_constant<int, 1>;
+  // a lane keeps a strip's old y and sums: 64 positions of bf16, 32 of fp32
+  if (!(ydt == QL_OUT_F32 ? (many ? expand(std::true_type{}, std::integral_constant<int, 2>{}) : expand(std::true_type{}, One{}))
+                          : (many ? expand(std::false_type{}, std::integral_constant<int, 4>{}) : expand(std::false_type{}, One{}))))
     return fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
   return launch_status("lora_add");
 }

@@ -371,17 +371,35 @@ def mdbf_select_rank(n, m, P, l, scale_bits, target_bits):
 
 # ------------------------------------------------------------------------------- rows grouped by an index
 
+# These run once or more per layer of a decode step, so that their checks are kept to a few attribute reads: every
+# tensor is compared with the device of the call's first one, which is checked against the current device.
+_LORA_ARRAYS = [None] + [LoraLayerC * n for n in range(1, 5)]
 _OUT = {torch.float32: QL_OUT_F32, torch.bfloat16: QL_OUT_BF16}
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+_cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _arg(t, dtype, what):
-    """Address of a contiguous CUDA tensor of one dtype on the current device (decode calls run once
-    per layer and step, so the checks are kept to a few attribute reads)."""
+def _device(t):
+    """The call's device, from its first tensor: the current CUDA device."""
+    d = t.get_device()
+    if d < 0 or d != _cuda_device():
+        _ptr(t)      # raises with the reason
+    return d
+
+
+def _arg(t, dtype, what, dev):
+    """Address of a contiguous tensor of one dtype on the call's device."""
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    return _any(t, what, dev)
+
+
+def _any(t, what, dev):
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return _ptr(t)
+    if t.get_device() != dev:
+        raise ValueError(f"tensor arguments must be CUDA tensors on cuda:{dev}, got {what} on {t.device}")
+    return t.data_ptr()
 
 
 def _out(t, what):
@@ -393,10 +411,14 @@ def _out(t, what):
     return d
 
 
-def _room(workspace):
+def _room(workspace, dev):
     if workspace is None:
         return None, 0
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return _any(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+
+
+def _on(stream, dev):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def group_rows(index, groups, order, offsets, workspace=None, stream=None):
@@ -405,11 +427,12 @@ def group_rows(index, groups, order, offsets, workspace=None, stream=None):
     with an index outside [0, groups) are in no group.  workspace: uint8 device tensor of at least
     group_rows_workspace_bytes(M, groups) bytes when that is non-zero."""
     M = index.numel()
-    if tuple(order.shape) != (M,) or index.dim() != 1 or tuple(offsets.shape) != (groups + 1,):
+    if order.shape != (M,) or index.dim() != 1 or offsets.shape != (groups + 1,):
         raise ValueError("index and order must be [M] and offsets [groups + 1]")
-    ws, nbytes = _room(workspace)
-    _check(_c("group_rows")(_arg(index, torch.int32, "index"), M, groups, _arg(order, torch.int32, "order"),
-                            _arg(offsets, torch.int32, "offsets"), ws, nbytes, _stream(stream)))
+    dev = _device(index)
+    ws, nbytes = _room(workspace, dev)
+    _check(_c("group_rows")(_arg(index, _I32, "index", dev), M, groups, _arg(order, _I32, "order", dev),
+                            _arg(offsets, _I32, "offsets", dev), ws, nbytes, _on(stream, dev)))
     return order, offsets
 
 
@@ -425,15 +448,15 @@ def moe_route(logits, experts, weights, order, offsets, normalize=True, workspac
     least moe_route_workspace_bytes(T, E, k) bytes when that is non-zero."""
     T, E = logits.shape
     k = experts.shape[1]
-    if tuple(experts.shape) != (T, k) or weights.shape != experts.shape:
+    if experts.shape != (T, k) or weights.shape != experts.shape:
         raise ValueError("experts and weights must be [T, k]")
-    if tuple(order.shape) != (T * k,) or tuple(offsets.shape) != (E + 1,):
+    if order.shape != (T * k,) or offsets.shape != (E + 1,):
         raise ValueError("order must be [T * k] and offsets [E + 1]")
-    ldt = _out(logits, "logits")
-    ws, nbytes = _room(workspace)
-    _check(_c("moe_route")(_ptr(logits), ldt, T, E, k, 1 if normalize else 0, _arg(experts, torch.int32, "experts"),
-                           _arg(weights, torch.float32, "weights"), _arg(order, torch.int32, "order"),
-                           _arg(offsets, torch.int32, "offsets"), ws, nbytes, _stream(stream)))
+    ldt, dev = _out(logits, "logits"), _device(logits)
+    ws, nbytes = _room(workspace, dev)
+    _check(_c("moe_route")(logits.data_ptr(), ldt, T, E, k, 1 if normalize else 0, _arg(experts, _I32, "experts", dev),
+                           _arg(weights, _F32, "weights", dev), _arg(order, _I32, "order", dev),
+                           _arg(offsets, _I32, "offsets", dev), ws, nbytes, _on(stream, dev)))
     return experts, weights, order, offsets
 
 
@@ -441,11 +464,10 @@ def moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
     return int(_c("moe_route_workspace_bytes")(T, E, k))
 
 
-def _groups_c(G, offsets, x, y, x_rows, x_div, y_rows):
+def _groups_c(G, offsets, x, y, x_rows, x_div, y_rows, dev):
     """ql_groups of a call: M positions come from x_rows or y_rows, or are the rows of x."""
-    if tuple(offsets.shape) != (G + 1,):
-        raise ValueError("offsets must be [G + 1]")
-    M = x.shape[0]
+    X = x.shape[0]
+    M, xp, yp = X, None, None
     if x_rows is not None:
         M = x_rows.numel()
     elif x_div != 1:
@@ -454,16 +476,19 @@ def _groups_c(G, offsets, x, y, x_rows, x_div, y_rows):
         if x_rows is not None and y_rows.numel() != M:
             raise ValueError("x_rows and y_rows must have one entry per position")
         M = y_rows.numel()
-    return GroupsC(_arg(offsets, torch.int32, "offsets"), None if x_rows is None else _arg(x_rows, torch.int32, "x_rows"),
-                   None if y_rows is None else _arg(y_rows, torch.int32, "y_rows"), x_div, G, M, x.shape[0], y.shape[0])
+        yp = _arg(y_rows, _I32, "y_rows", dev)
+    if x_rows is not None:
+        xp = _arg(x_rows, _I32, "x_rows", dev)
+    return GroupsC(_arg(offsets, _I32, "offsets", dev), xp, yp, x_div, G, M, X, y.shape[0])
 
 
 def _grouped_layer(codes, lut, K, what):
     G, N, B = codes.shape
     if B * 4 != 3 * K:
         raise ValueError(f"{what} codes must be [G, N, 3K/4]")
-    if lut.dtype not in (torch.bfloat16, torch.int16) or tuple(lut.shape) != (G, N, 64) or not lut.is_contiguous():
+    if lut.dtype not in (_BF16, torch.int16) or lut.shape != (G, N, 64) or not lut.is_contiguous():
         raise TypeError(f"{what} lut must be a contiguous bf16 [G, N, 64] tensor")
+    return G, N
 
 
 def benq_grouped_linear(codes, lut, x, offsets, y, x_rows=None, x_div=1, y_rows=None, stream=None):
@@ -474,34 +499,38 @@ def benq_grouped_linear(codes, lut, x, offsets, y, x_rows=None, x_div=1, y_rows=
     yr(i) = y_rows[i] (no row twice), or i without y_rows; both int32 [M].  With moe_route's plan of k
     slots per token: x_rows=order, x_div=k reads token rows and writes sorted rows; y_rows=order reads
     sorted rows and writes slots."""
-    K = x.shape[1]
-    G, N = codes.shape[:2]
-    _grouped_layer(codes, lut, K, "the")
+    X, K = x.shape
+    G, N = _grouped_layer(codes, lut, K, "the")
     ydt = _out(y, "y")
     if y.dim() != 2 or y.shape[1] != N:
         raise ValueError("y must be [Y, N]")
-    g = _groups_c(G, offsets, x, y, x_rows, x_div, y_rows)
-    _check(_c("benq_grouped_linear")(_arg(codes, torch.uint8, "codes"), _ptr(lut), g, _arg(x, torch.bfloat16, "x"),
-                                     _ptr(y), ydt, N, K, _stream(stream)))
+    if offsets.shape != (G + 1,):
+        raise ValueError("offsets must be [G + 1]")
+    dev = _device(x)
+    g = _groups_c(G, offsets, x, y, x_rows, x_div, y_rows, dev)
+    _check(_c("benq_grouped_linear")(_arg(codes, _U8, "codes", dev), _any(lut, "lut", dev), g, _arg(x, _BF16, "x", dev),
+                                     _any(y, "y", dev), ydt, N, K, _on(stream, dev)))
     return y
 
 
 def benq_grouped_gate_up(codes_g, lut_g, codes_u, lut_u, x, offsets, h, x_rows=None, x_div=1, y_rows=None, stream=None):
     """h[yr(i)] = silu(x[xr(i)] @ W_g^T) * (x[xr(i)] @ W_u^T) with the two layers of position i's group;
     arguments as benq_grouped_linear, h float32 or bf16 [Y, N]."""
-    K = x.shape[1]
-    G, N = codes_g.shape[:2]
-    _grouped_layer(codes_g, lut_g, K, "gate")
+    X, K = x.shape
+    G, N = _grouped_layer(codes_g, lut_g, K, "gate")
     if codes_u.shape != codes_g.shape:
         raise ValueError("gate and up codes must have one shape")
     _grouped_layer(codes_u, lut_u, K, "up")
     hdt = _out(h, "h")
     if h.dim() != 2 or h.shape[1] != N:
         raise ValueError("h must be [Y, N]")
-    g = _groups_c(G, offsets, x, h, x_rows, x_div, y_rows)
-    _check(_c("benq_grouped_gate_up")(_arg(codes_g, torch.uint8, "gate codes"), _ptr(lut_g),
-                                      _arg(codes_u, torch.uint8, "up codes"), _ptr(lut_u), g,
-                                      _arg(x, torch.bfloat16, "x"), _ptr(h), hdt, N, K, _stream(stream)))
+    if offsets.shape != (G + 1,):
+        raise ValueError("offsets must be [G + 1]")
+    dev = _device(x)
+    g = _groups_c(G, offsets, x, h, x_rows, x_div, y_rows, dev)
+    _check(_c("benq_grouped_gate_up")(_arg(codes_g, _U8, "gate codes", dev), _any(lut_g, "gate lut", dev),
+                                      _arg(codes_u, _U8, "up codes", dev), _any(lut_u, "up lut", dev), g,
+                                      _arg(x, _BF16, "x", dev), _any(h, "h", dev), hdt, N, K, _on(stream, dev)))
     return h
 
 
@@ -510,17 +539,19 @@ def moe_combine(y, experts, weights, out, residual=None, stream=None):
     (j ascending, fp32).  y float32 or bf16 [T * k, N]; experts int32, weights float32 [T, k]; out and
     residual (optional, may be out itself) float32 or bf16 [T, N] of one dtype."""
     T, k = experts.shape
-    N = out.shape[1]
-    if tuple(y.shape) != (T * k, N) or weights.shape != experts.shape or out.shape[0] != T:
+    rows, N = y.shape
+    if rows != T * k or weights.shape != experts.shape or out.shape != (T, N):
         raise ValueError("y must be [T * k, N], weights [T, k] and out [T, N]")
     ydt, odt = _out(y, "y"), _out(out, "out")
-    res = None
     if residual is not None:
         if residual.shape != out.shape:
             raise ValueError("residual must be [T, N]")
-        res = _arg(residual, out.dtype, "residual")
-    _check(_c("moe_combine")(_ptr(y), ydt, _arg(experts, torch.int32, "experts"), _arg(weights, torch.float32, "weights"),
-                             res, _ptr(out), odt, T, k, N, _stream(stream)))
+        if residual.dtype is not out.dtype:
+            raise TypeError("residual must be of out's dtype")
+    dev = _device(y)
+    _check(_c("moe_combine")(y.data_ptr(), ydt, _arg(experts, _I32, "experts", dev), _arg(weights, _F32, "weights", dev),
+                             None if residual is None else _any(residual, "residual", dev), _any(out, "out", dev), odt,
+                             T, k, N, _on(stream, dev)))
     return out
 
 
@@ -537,24 +568,26 @@ def lora_add(layers, x, order, offsets, scale=None, workspace=None, stream=None)
         raise ValueError("lora_add takes 1 to 4 layers")
     T, K = x.shape
     G, r, _ = layers[0][0].shape
-    ydt = _out(layers[0][2], "y")
-    arr = (LoraLayerC * S)()
+    ydt = layers[0][2].dtype
     for A, B, y in layers:
         N = B.shape[1]
-        if tuple(A.shape) != (G, r, K) or tuple(B.shape) != (G, N, r):
+        if A.shape != (G, r, K) or B.shape != (G, N, r):
             raise ValueError("A must be [G, r, K] and B [G, N, r], with one G and r")
-        if tuple(y.shape) != (T, N) or _out(y, "y") != ydt:
+        if y.shape != (T, N) or y.dtype is not ydt or not y.is_contiguous():
             raise ValueError("each y must be contiguous [T, N] of the first y's dtype")
-    if tuple(order.shape) != (T,) or tuple(offsets.shape) != (G + 1,):
+    if order.shape != (T,) or offsets.shape != (G + 1,):
         raise ValueError("order must be [T] and offsets [G + 1]")
-    if scale is not None and tuple(scale.shape) != (G,):
+    if scale is not None and scale.shape != (G,):
         raise ValueError("scale must be [G]")
+    ydt, dev = _out(y, "y"), _device(x)
+    arr = _LORA_ARRAYS[S]()
     for i, (A, B, y) in enumerate(layers):
-        arr[i] = LoraLayerC(_arg(A, torch.bfloat16, "A"), _arg(B, torch.bfloat16, "B"), _ptr(y), B.shape[1])
-    ws, nbytes = _room(workspace)
-    _check(_c("lora_add")(arr, S, _arg(x, torch.bfloat16, "x"), _arg(order, torch.int32, "order"),
-                          _arg(offsets, torch.int32, "offsets"), None if scale is None else _arg(scale, torch.float32, "scale"),
-                          ydt, G, T, r, K, ws, nbytes, _stream(stream)))
+        c = arr[i]
+        c.A, c.B, c.y, c.N = _arg(A, _BF16, "A", dev), _arg(B, _BF16, "B", dev), _any(y, "y", dev), B.shape[1]
+    ws, nbytes = _room(workspace, dev)
+    _check(_c("lora_add")(arr, S, _arg(x, _BF16, "x", dev), _arg(order, _I32, "order", dev),
+                          _arg(offsets, _I32, "offsets", dev), None if scale is None else _arg(scale, _F32, "scale", dev),
+                          ydt, G, T, r, K, ws, nbytes, _on(stream, dev)))
     return [y for _, _, y in layers]
 
 

@@ -18,6 +18,8 @@ constexpr int CHUNK_ONE = 4096;    // keys one CTA places in a single launch
 constexpr int CHUNK_MIN = 1024;    // keys per CTA otherwise, more when that would take over CHUNKS_MAX CTAs
 constexpr int CHUNKS_MAX = 256;
 constexpr int ONE_TOKENS = 64;     // tokens the router handles in a single launch
+constexpr int ROUTE_MIN = 32;      // tokens per CTA otherwise: one per warp while the chunks stay few
+constexpr int PLACE_THREADS = 1024;
 constexpr unsigned FULL = 0xffffffffu;
 
 struct Chunks {
@@ -29,11 +31,11 @@ Chunks chunks_of(int M) {
   return {size, (M + size - 1) / size};
 }
 Chunks token_chunks_of(int T) {   // tokens per CTA of the router
-  const int size = std::max(ONE_TOKENS, (T + CHUNKS_MAX - 1) / CHUNKS_MAX);
+  const int size = std::max(ROUTE_MIN, (T + CHUNKS_MAX - 1) / CHUNKS_MAX);
   return {size, (T + size - 1) / size};
 }
 
-size_t scatter_smem(int warps, int G) { return (size_t)(warps + 1) * G * sizeof(int) + 16; }
+size_t scatter_smem(int G) { return (size_t)(PLACE_THREADS / 32 + 2) * G * sizeof(int) + 16; }
 
 __device__ __forceinline__ int key_of(const int32_t *index, int i, int end, int G) {
   if (i >= end) return -1;
@@ -47,10 +49,12 @@ __device__ void place_chunk(const int32_t *index, int M, int G, int s0, int s1, 
                             int chunk, int32_t *__restrict__ order, int32_t *__restrict__ offsets,
                             unsigned char *smem) {
   int *base = reinterpret_cast<int *>(smem);                                   // [G + 1]
-  int *wh = base + G + 4;                                                      // [warps][G]
+  int *before = base + G + 4;                                                  // [G]
+  int *wh = before + G;                                                        // [warps][G]
   const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int *mine = wh + (size_t)warp * G;
   for (int i = threadIdx.x; i < nw * G; i += blockDim.x) wh[i] = 0;
+  for (int g = threadIdx.x; g < G; g += blockDim.x) base[g] = before[g] = 0;
   const int run = ((s1 - s0 + nw - 1) / nw + 31) / 32 * 32;
   const int r0 = min(s1, s0 + warp * run), r1 = min(s1, r0 + run);
   __syncthreads();
@@ -61,7 +65,8 @@ __device__ void place_chunk(const int32_t *index, int M, int G, int s0, int s1, 
     __syncwarp();
   }
   __syncthreads();
-  // per group: the runs' counts become starts within the chunk; base gets the total over all chunks
+  // per group: the runs' counts become starts within the chunk; base gets the total over all chunks, before the sum of
+  // the chunks in front of this one
   for (int g = threadIdx.x; g < G; g += blockDim.x) {
     int sum = 0;
     for (int w = 0; w < nw; ++w) {
@@ -69,11 +74,21 @@ __device__ void place_chunk(const int32_t *index, int M, int G, int s0, int s1, 
       wh[(size_t)w * G + g] = sum;
       sum += c;
     }
-    if (hist) {
-      sum = 0;
-      for (int c = 0; c < nchunks; ++c) sum += __ldcg(hist + (size_t)c * G + g);
+    if (!hist) base[g] = sum;
+  }
+  if (hist) {   // threads share out (chunk, group) pairs, so that a few loads in flight per thread cover them all
+    const int g32 = (G + 31) / 32 * 32, segs = max(1, (int)blockDim.x / g32);
+    for (int g = threadIdx.x % g32, seg = threadIdx.x / g32; g < G && seg < segs; g += g32) {
+      int all = 0, mine_before = 0;
+#pragma unroll 16
+      for (int c = seg; c < nchunks; c += segs) {
+        const int v = __ldcg(hist + (size_t)c * G + g);
+        all += v;
+        if (c < chunk) mine_before += v;
+      }
+      atomicAdd(base + g, all);            // integer sums: the order does not matter
+      atomicAdd(before + g, mine_before);
     }
-    base[g] = sum;
   }
   __syncthreads();
   if (warp == 0) {   // exclusive sum over the groups
@@ -96,20 +111,11 @@ __device__ void place_chunk(const int32_t *index, int M, int G, int s0, int s1, 
   if (chunk == 0)
     for (int g = threadIdx.x; g <= G; g += blockDim.x) offsets[g] = base[g];
   const int total = base[G];
-  if (hist) {   // this chunk's start within each group
-    __syncthreads();
-    for (int g = threadIdx.x; g < G; g += blockDim.x) {
-      int before = 0;
-      for (int c = 0; c < chunk; ++c) before += __ldcg(hist + (size_t)c * G + g);
-      base[g] += before;
-    }
-    __syncthreads();
-  }
   for (int i = r0; i < r1; i += 32) {
     const int key = key_of(index, i + lane, r1, G);
     const unsigned same = __match_any_sync(FULL, key);
     int at = -1;
-    if (key >= 0) at = base[key] + mine[key] + __popc(same & ((1u << lane) - 1));
+    if (key >= 0) at = base[key] + before[key] + mine[key] + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
     if (at >= 0) order[at] = i + lane;
@@ -245,9 +251,9 @@ template <int V>
 void launch_route(const void *logits, ql_out_dtype ldt, int T, int E, int k, int normalize, int32_t *experts,
                   float *weights, int *hist, int32_t *order, int32_t *offsets, cudaStream_t s) {
   if (T <= ONE_TOKENS) {
-    const size_t smem = scatter_smem(32, E);
+    const size_t smem = scatter_smem(E);
     if (smem > 40 * 1024) (void)ql::set_max_smem(moe_route_kernel<V, true>, (int)smem);
-    ql::launch(moe_route_kernel<V, true>, 1, 1024, smem, s, logits, (int)ldt, T, E, k, normalize, T, experts, weights,
+    ql::launch(moe_route_kernel<V, true>, 1, PLACE_THREADS, smem, s, logits, (int)ldt, T, E, k, normalize, T, experts, weights,
                hist, order, offsets);
   } else {
     const Chunks c = token_chunks_of(T);
@@ -259,10 +265,9 @@ void launch_route(const void *logits, ql_out_dtype ldt, int T, int E, int k, int
 // the second launch: places the keys of every chunk
 void launch_place(const int32_t *index, int M, int G, Chunks c, const int *hist, int32_t *order, int32_t *offsets,
                   cudaStream_t s) {
-  const int threads = hist ? 256 : 1024;
-  const size_t smem = scatter_smem(threads / 32, G);
+  const size_t smem = scatter_smem(G);
   if (smem > 40 * 1024) (void)ql::set_max_smem(group_place_kernel, (int)smem);
-  ql::launch(group_place_kernel, std::max(1, c.count), threads, smem, s, index, M, G, c.size, hist, c.count, order,
+  ql::launch(group_place_kernel, std::max(1, c.count), PLACE_THREADS, smem, s, index, M, G, c.size, hist, c.count, order,
              offsets);
 }
 

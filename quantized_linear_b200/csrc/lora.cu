@@ -17,11 +17,13 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ql_internal.cuh"
+#include "lora.cuh"
 
 namespace {
 
-constexpr int MAX_LAYERS = 4;
+using lora::find_tile;
+using lora::Layers;
+
 constexpr int ST = 32;               // positions per shrink tile
 constexpr int RT = 64;               // positions per shrink tile of the ring form
 constexpr int RK = 64;               // inputs per stage of its ring
@@ -29,46 +31,6 @@ constexpr int RSTAGES = 4;
 constexpr int EF = 256;              // features per round of an expand CTA: 8 warps x a strip of 32
 constexpr int KS_MAX = 8;            // CTAs that share K
 constexpr int WARPS = 8;
-constexpr unsigned FULL = 0xffffffffu;
-
-struct Layers {
-  const uint16_t *A[MAX_LAYERS], *B[MAX_LAYERS];
-  void *y[MAX_LAYERS];
-  int N[MAX_LAYERS];
-  int chunk0[MAX_LAYERS + 1];        // expand: CTAs (runs of feature rounds) before each layer
-};
-
-// The tile'th tile of `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
-__device__ __forceinline__ void find_tile(const int32_t *offsets, int G, int T, int tt, int tile, int &g, int &p0, int &p1) {
-  const int lane = threadIdx.x & 31;
-  g = -1;
-  int carry = 0;
-  for (int g0 = 0; g0 < G; g0 += 32) {
-    int a = 0, b = 0;
-    if (g0 + lane < G) {
-      a = max(0, min(T, __ldcg(offsets + g0 + lane)));
-      b = max(a, min(T, __ldcg(offsets + g0 + lane + 1)));
-    }
-    const int n = (b - a + tt - 1) / tt;
-    int s = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(FULL, s, d);
-      if (lane >= d) s += u;
-    }
-    const bool mine = tile >= carry + s - n && tile < carry + s;
-    const unsigned who = __ballot_sync(FULL, mine);
-    if (who) {
-      const int src = __ffs(who) - 1;
-      const int at = a + (tile - (carry + s - n)) * tt;
-      g = g0 + src;
-      p0 = __shfl_sync(FULL, at, src);
-      p1 = min(__shfl_sync(FULL, b, src), p0 + tt);
-      return;
-    }
-    carry += __shfl_sync(FULL, s, 31);
-  }
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -307,12 +269,13 @@ __device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int r, bool v
 }
 
 // Tiles of 16 MTL positions; grid (runs of `rounds` feature rounds of all layers, tiles).  The y values of a strip are
-// requested before its products, so that the two overlap.
+// requested before its products, so that the two overlap; B's rows come straight from memory, KC blocks of 16 ranks
+// at a time, the first of them before t is prepared.
 template <bool F32, int MTL>
-__global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 4 : 2)
+__global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
     lora_expand_kernel(const Layers L, int S, const int32_t *order, const int32_t *offsets, const float *scale, int G,
                        int T, int r, int shares, int rounds, const float *t) {
-  constexpr int ET = 16 * MTL;
+  constexpr int ET = 16 * MTL, KC = MTL == 1 ? 4 : 1;
   extern __shared__ __align__(16) unsigned char esm[];   // t as bf16: [hi, lo][ET][rp], rows of rp * 2 bytes
   __shared__ int where[3], rows[ET];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -335,9 +298,40 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 4 : 2)
   if (g < 0) return;
   int s = 0;
   while (s + 1 < S && (int)blockIdx.x >= L.chunk0[s + 1]) ++s;
-  const int N = L.N[s], f0 = ((int)blockIdx.x - L.chunk0[s]) * rounds * EF + 32 * warp;
+  const int N = L.N[s], f0 = ((int)blockIdx.x - L.chunk0[s]) * rounds * EF;
+  const uint16_t *const B = L.B[s] + (int64_t)g * N * r;
   const int mt = MTL == 1 ? 1 : (count + 15) / 16;
+  const bool vec = r % 4 == 0;                    // 8-byte aligned rows of B
+  const bool whole = N % 8 == 0;                  // 16-byte aligned pieces of y, none partial
   uint16_t *hi = reinterpret_cast<uint16_t *>(esm), *lo = hi + ET * rp;
+  // MMA column c of the strip's tile i is feature n0 + 8 (c / 2) + 2 i + c % 2
+  uint2 b[KC][4];
+  auto load_b = [&](int n0, int k0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = n0 + 8 * (gid >> 1) + 2 * i + (gid & 1);
+#pragma unroll
+      for (int k = 0; k < KC; ++k) b[k][i] = load4(c < N ? B + (int64_t)c * r : nullptr, 16 * (k0 + k) + 4 * tig, r, vec);
+    }
+  };
+  // this lane's old outputs of a strip: features n .. n + 7 of positions gid and gid + 8 of each 16
+  uint4 old[MTL][2][F32 ? 2 : 1];
+  auto load_y = [&](int n) {
+    if (whole && n < N) {
+#pragma unroll
+      for (int m = 0; m < MTL; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = rows[16 * m + 8 * h + gid];
+          if (row < 0) continue;
+          const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const char *>(L.y[s]) + ((size_t)row * N + n) * (F32 ? 4 : 2));
+#pragma unroll
+          for (int i = 0; i < (F32 ? 2 : 1); ++i) old[m][h][i] = __ldcg(v + i);
+        }
+    }
+  };
+  if constexpr (KC > 1) load_b(f0 + 32 * warp, 0);
+  load_y(f0 + 32 * warp + 8 * tig);
   const float f = scale ? __ldcg(scale + g) : 1.f;
   for (int i = threadIdx.x; i < mt * 16 * r16 * 16; i += WARPS * 32) {
     const int p = i / (r16 * 16), j = i - p * (r16 * 16);
@@ -356,51 +350,32 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 4 : 2)
     lo[p * rp + at] = (rest == rest) ? qld::f32_to_bf16_rn(rest) : 0;   // inf and NaN are in hi alone
   }
   __syncthreads();
-  const bool vec = r % 4 == 0;                    // 8-byte aligned rows of B
-  const bool whole = N % 8 == 0;                  // 16-byte aligned pieces of y, none partial
   const uint32_t frag = static_cast<uint32_t>(__cvta_generic_to_shared(hi)) + ((lane & 15) * rp + (lane >> 4) * 8) * 2;
   for (int rd = 0; rd < rounds; ++rd) {
-    const int n0 = f0 + rd * EF;
-    if (n0 >= N) return;
-    const int n = n0 + 8 * tig;                   // this lane's features n .. n + 7, of positions gid and gid + 8 of each 16
-    uint4 old[MTL][2][F32 ? 2 : 1];
-    if (whole && n < N) {
-#pragma unroll
-      for (int m = 0; m < MTL; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = rows[16 * m + 8 * h + gid];
-          if (row < 0) continue;
-          const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const char *>(L.y[s]) + ((size_t)row * N + n) * (F32 ? 4 : 2));
-#pragma unroll
-          for (int i = 0; i < (F32 ? 2 : 1); ++i) old[m][h][i] = __ldcg(v + i);
-        }
-    }
-    // MMA column c of the strip's tile i is feature n0 + 8 (c / 2) + 2 i + c % 2
-    const uint16_t *br[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = n0 + 8 * (gid >> 1) + 2 * i + (gid & 1);
-      br[i] = c < N ? L.B[s] + ((int64_t)g * N + c) * r : nullptr;
-    }
+    const int n0 = f0 + rd * EF + 32 * warp, n = n0 + 8 * tig;
+    if (f0 + rd * EF >= N) break;
+    if (rd > 0) load_y(n);
     float acc[MTL][4][4] = {};
-#pragma unroll 2
-    for (int k = 0; k < r16; ++k) {
-      uint2 b[4];
+    for (int k0 = 0; k0 < r16; k0 += KC) {
+      if (KC == 1 || rd > 0 || k0 > 0) {
+        load_b(n0, k0);
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = load4(br[i], 16 * k + 4 * tig, r, vec);
+      for (int k = 0; k < KC; ++k) {
+        if (k0 + k >= r16) break;
 #pragma unroll
-      for (int m = 0; m < MTL; ++m)
-        if (m < mt) {
-          uint32_t ah[4], al[4];
-          ldmatrix_x4(frag + (16 * m * rp + 16 * k) * 2, ah);
-          ldmatrix_x4(frag + ((ET + 16 * m) * rp + 16 * k) * 2, al);
+        for (int m = 0; m < MTL; ++m)
+          if (m < mt) {
+            uint32_t ah[4], al[4];
+            ldmatrix_x4(frag + (16 * m * rp + 16 * (k0 + k)) * 2, ah);
+            ldmatrix_x4(frag + ((ET + 16 * m) * rp + 16 * (k0 + k)) * 2, al);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mma16816(acc[m][i], al[0], al[1], al[2], al[3], b[i].x, b[i].y);
-            mma16816(acc[m][i], ah[0], ah[1], ah[2], ah[3], b[i].x, b[i].y);
+            for (int i = 0; i < 4; ++i) {
+              mma16816(acc[m][i], al[0], al[1], al[2], al[3], b[k][i].x, b[k][i].y);
+              mma16816(acc[m][i], ah[0], ah[1], ah[2], ah[3], b[k][i].x, b[k][i].y);
+            }
           }
-        }
+      }
     }
     if (n >= N) continue;
 #pragma unroll
@@ -471,8 +446,13 @@ ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, co
                           const int32_t *offsets, const float *scale, ql_out_dtype ydt, int G, int T, int r, int K,
                           void *ws, cudaStream_t s) {
   const bool many = many_rows(G, T), ring = many && K % 8 == 0;
-  // feature rounds per expand CTA: t is prepared once for them; few tiles need the CTAs
-  const int rounds = many && T >= 1024 ? 4 : 1;
+  // feature rounds per expand CTA, which prepares t once for them: two CTAs per SM in all; t of 16 positions is little,
+  // and more CTAs in flight count for more (q, k, v of 32 rows: 6.6 us, 8.6 with two rounds)
+  const int et = many ? (ydt == QL_OUT_F32 ? 32 : 64) : 16;
+  int64_t all = 0;
+  for (int i = 0; i < S; ++i) all += (layers[i].N + EF - 1) / EF;
+  all *= std::min(G, T) + T / et;
+  const int rounds = !many ? 1 : (int)std::max<int64_t>(1, (all + 2 * sm_count() - 1) / (2 * sm_count()));
   Layers L{};
   for (int i = 0; i < S; ++i) {
     L.A[i] = layers[i].A;
@@ -500,6 +480,8 @@ ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, co
         : r <= 32 ? by_rank(std::integral_constant<int, 2>{})
                   : by_rank(std::integral_constant<int, 4>{})))
     return fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
+  if (many && lora::expand_mma_takes(L, S, G, T, r))
+    return lora::expand_mma_launch(L, S, order, offsets, scale, ydt, G, T, r, shares, t, s);
   auto expand = [&](auto f32c, auto mtl) -> bool {
     constexpr int ET = 16 * decltype(mtl)::value;
     auto kern = lora_expand_kernel<decltype(f32c)::value, decltype(mtl)::value>;

@@ -1,0 +1,56 @@
+// Shared by the adapter kernels (lora.cu, lora_sm100.cu); not part of the ABI.
+#pragma once
+
+#include "ql_internal.cuh"
+
+namespace lora {
+
+constexpr int MAX_LAYERS = 4;
+
+struct Layers {
+  const uint16_t *A[MAX_LAYERS], *B[MAX_LAYERS];
+  void *y[MAX_LAYERS];
+  int N[MAX_LAYERS];
+  int chunk0[MAX_LAYERS + 1];        // expand: feature chunks (or runs of them) before each layer
+};
+
+// The tile'th tile of `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
+// Returns the number of tiles before the group that it stopped at (with tile past the last: the number of all tiles).
+__device__ __forceinline__ int find_tile(const int32_t *offsets, int G, int T, int tt, int tile, int &g, int &p0, int &p1) {
+  const int lane = threadIdx.x & 31;
+  g = -1;
+  int carry = 0;
+  for (int g0 = 0; g0 < G; g0 += 32) {
+    int a = 0, b = 0;
+    if (g0 + lane < G) {
+      a = max(0, min(T, __ldcg(offsets + g0 + lane)));
+      b = max(a, min(T, __ldcg(offsets + g0 + lane + 1)));
+    }
+    const int n = (b - a + tt - 1) / tt;
+    int s = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += u;
+    }
+    const bool mine = tile >= carry + s - n && tile < carry + s;
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      const int at = a + (tile - (carry + s - n)) * tt;
+      g = g0 + src;
+      p0 = __shfl_sync(0xffffffffu, at, src);
+      p1 = min(__shfl_sync(0xffffffffu, b, src), p0 + tt);
+      return carry;
+    }
+    carry += __shfl_sync(0xffffffffu, s, 31);
+  }
+  return carry;
+}
+
+// The expand stage on the tensor cores (lora_sm100.cu): whether it takes these sizes, and its launch.
+bool expand_mma_takes(const Layers &L, int S, int G, int T, int r);
+ql_status expand_mma_launch(const Layers &L, int S, const int32_t *order, const int32_t *offsets, const float *scale,
+                            ql_out_dtype ydt, int G, int T, int r, int shares, const float *t, cudaStream_t s);
+
+}  // namespace lora

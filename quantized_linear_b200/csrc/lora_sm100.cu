@@ -1,0 +1,374 @@
+// The adapters' expand stage for many rows per adapter, on the tensor cores:
+//   y[i][n] += sum_j B_g[n][j] t[i][j] for 128 positions of one adapter by 256 features at a time.
+//
+// What it cannot do without is y, read and written once (4 bytes per output in bf16).  On the warp MMA the products of
+// the pair t = hi + lo alone take as long as that traffic (447 TFLOP/s measured) and their operands' loads longer;
+// here they cost the issuing threads nothing.  A CTA (17 warps, one per SM) walks a run of
+// (layer, tile, 256 features) units, runs of equal length over the actual tiles:
+//   * warp 16 loads B's rows by tensor copies (two stages) and issues the MMAs, a unit ahead: M = 128 positions,
+//     N = 256 features, K = r twice (hi, then lo, against the same B), into two accumulators of 256 columns;
+//   * warps 0-15 prepare t when the tile changes (sum of the K shares in order, scale, hi + lo, 128-byte swizzled rows), request
+//     the unit's y values, and add the accumulators to them.
+// The copy's five dimensions (k, feature bit 0, bits 3-4, bits 1-2, the rest) permute the features of each 32 so that
+// a lane's accumulator fragments (tcgen05.ld 16x256b: two columns of each eight) are 8 consecutive features: 16-byte
+// loads and stores of a bf16 y.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "lora.cuh"
+#include "pair_gemm.cuh"
+#include "sm100_ptx.cuh"
+
+namespace {
+
+using namespace pairgemm;
+using lora::Layers;
+using lora::MAX_LAYERS;
+
+constexpr int TM = 128, TN = 256;            // positions and features of a unit
+constexpr int WORK = 16;                     // epilogue warps
+constexpr int THREADS = (WORK + 1) * 32;
+constexpr int RMAX = 128;                    // ranks (two 64-wide blocks of t and of each B stage fit)
+constexpr int BST = 2;                       // B stages
+
+__device__ int g_lora_timeout = 0;
+
+struct Maps {
+  CUtensorMap b[MAX_LAYERS];
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int x, int strip, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(0), "r"(strip), "r"(bar)
+      : "memory");
+}
+
+// 16 lanes x 32 columns as fragments: r[4 j + 0, 1]: lane (thread / 4), columns 8 j + 2 (thread % 4) + 0, 1; r[4 j + 2, 3]:
+// lane + 8
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(THREADS, 1)
+    lora_expand_mma_kernel(const __grid_constant__ Maps maps, const Layers L, int S, const int32_t *order,
+                           const int32_t *offsets, const float *scale, int G, int T, int r, int shares, const float *t) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ int rows[TM], where[4];
+  __shared__ __align__(8) uint64_t bars[2 * BST + 6];
+  __shared__ uint32_t tmem_word, abort_word;
+  const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+  const uint32_t tb = (raw + 1023u) & ~1023u;            // t: [hi, lo][64-wide block][128 rows x 128 bytes]
+  const int kch = (r + 63) / 64;
+  const uint32_t bbytes = kch * TN * 128;
+  const uint32_t bb = tb + 2 * kch * TM * 128;           // B: [stage][block][256 rows x 128 bytes]
+  const uint32_t b_full = static_cast<uint32_t>(__cvta_generic_to_shared(bars)), b_free = b_full + 8 * BST;
+  const uint32_t d_full = b_free + 8 * BST, d_free = d_full + 16, t_full = d_free + 16, meet = t_full + 8;
+  const uint32_t tslot = static_cast<uint32_t>(__cvta_generic_to_shared(&tmem_word));
+  const uint32_t aslot = static_cast<uint32_t>(__cvta_generic_to_shared(&abort_word));
+  const Waiter wt{aslot, sm100::mapa_shared(aslot, 0)};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool ok = true;
+  auto warp_wait = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wt.wait(b, parity, false)) != 0; };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < BST; ++i) {
+      sm100::mbar_init(b_full + 8 * i, 1);
+      sm100::mbar_init(b_free + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(d_full + 8 * i, 1);
+      sm100::mbar_init(d_free + 8 * i, WORK);
+    }
+    sm100::mbar_init(t_full, WORK);
+    sm100::mbar_init(meet, WORK);
+    abort_word = 0;
+    sm100::fence_barrier_init();
+  }
+  if (warp == WORK) {
+    __syncwarp();
+    sm100::tmem_alloc(tslot, 512);
+    sm100::tmem_relinquish();
+  }
+  qld::pdl_trigger();
+  qld::pdl_wait();
+  if (warp == 0) {                                       // how many tiles there are
+    int g, p0, p1;
+    const int n = lora::find_tile(offsets, G, T, TM, 0x7fffffff, g, p0, p1);
+    if (lane == 0) where[3] = n;
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&tmem_word);
+  const int tiles = where[3];
+  const int64_t units = (int64_t)tiles * L.chunk0[S];    // layer after layer: tiles x 256-feature chunks
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  struct Unit {
+    int s, ti, c;
+  };
+  auto unit_at = [&](int64_t u) {
+    Unit v{0, 0, 0};
+    while (v.s + 1 < S && u >= (int64_t)tiles * L.chunk0[v.s + 1]) ++v.s;
+    const int chunks = L.chunk0[v.s + 1] - L.chunk0[v.s];
+    const int w = (int)(u - (int64_t)tiles * L.chunk0[v.s]);
+    v.ti = w / chunks;
+    v.c = w - v.ti * chunks;
+    return v;
+  };
+
+  if (warp == WORK) {
+    // ------------------------------------------------------------ B copies and MMAs
+    const uint32_t idesc = sm100::idesc_bf16_f32(TM, TN);
+    int ft = -1, fg = -1;                                // the tile last fetched for, its adapter
+    auto fetch = [&](int64_t u) {
+      if (u >= u1) return true;
+      const Unit v = unit_at(u);
+      if (v.ti != ft) {
+        int p0, p1;
+        lora::find_tile(offsets, G, T, TM, v.ti, fg, p0, p1);
+        ft = v.ti;
+      }
+      const int64_t k = u - u0;
+      const int st = (int)(k % BST);
+      if (k >= BST && !warp_wait(b_free + 8 * st, ((k / BST) & 1) ^ 1)) return false;
+      if (sm100::elect_one()) {
+        sm100::mbar_arrive_expect_tx(b_full + 8 * st, bbytes);
+        const int strip = (int)(((int64_t)fg * L.N[v.s] + (int64_t)v.c * TN) / 32);
+        for (int b = 0; b < kch; ++b)
+          tma_load_5d(bb + st * bbytes + b * TN * 128, &maps.b[v.s], 64 * b, strip, b_full + 8 * st);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int i = 0; i < BST && ok; ++i) ok = fetch(u0 + i);
+    int ps = -1, pt = -1, prepared = 0;
+    for (int64_t u = u0; u < u1 && ok; ++u) {
+      const int64_t k = u - u0;
+      const int st = (int)(k % BST), d = (int)(k & 1);
+      const Unit v = unit_at(u);
+      if (v.s != ps || v.ti != pt) {
+        ps = v.s;
+        pt = v.ti;
+        if (!warp_wait(t_full, prepared & 1)) { ok = false; break; }
+        ++prepared;
+      }
+      if (!warp_wait(b_full + 8 * st, (k / BST) & 1) || (k >= 2 && !warp_wait(d_free + 8 * d, ((k >> 1) & 1) ^ 1))) {
+        ok = false;
+        break;
+      }
+      sm100::tc_fence_after();
+      if (sm100::elect_one()) {
+        uint32_t add = 0;
+        for (int h = 1; h >= 0; --h)                     // lo first
+          for (int b = 0; b < kch; ++b) {
+            const uint64_t ad = sm100::sw128_kmajor_desc(tb + (h * kch + b) * TM * 128);
+            const uint64_t bd = sm100::sw128_kmajor_desc(bb + st * bbytes + b * TN * 128);
+            const int steps = min(4, (r - 64 * b + 15) / 16);
+            for (int kk = 0; kk < steps; ++kk) {
+              sm100::mma_bf16(tmem + d * TN, ad + 2 * kk, bd + 2 * kk, idesc, add);
+              add = 1;
+            }
+          }
+        sm100::mma_commit(b_free + 8 * st);
+        sm100::mma_commit(d_full + 8 * d);
+      }
+      __syncwarp();
+      ok = fetch(u + BST);
+    }
+  } else {
+    // ------------------------------------------------------------ t, then y
+    const int q = warp & 3, part = warp >> 2;            // tensor-memory quarter (32 positions), 64 of the 256 features
+    const int gid = lane >> 2, tig = lane & 3, r16 = (r + 15) / 16 * 16;
+    int ps = -1, pt = -1;
+    uint32_t met = 0;
+    // all worker warps meet (a bounded wait: none is left behind by one that gave up)
+    auto together = [&]() {
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(meet);
+      return warp_wait(meet, met++ & 1);
+    };
+    for (int64_t u = u0; u < u1; ++u) {
+      const int64_t k = u - u0;
+      const int d = (int)(k & 1);
+      const Unit v = unit_at(u);
+      const int N = L.N[v.s];
+      if (v.s != ps || v.ti != pt) {
+        ps = v.s;
+        pt = v.ti;
+        // every warp is past its last unit, whose MMAs are done: t and rows may be rewritten
+        if (!together()) { ok = false; break; }
+        if (warp == 0) {
+          int g, p0 = 0, p1 = 0;
+          lora::find_tile(offsets, G, T, TM, v.ti, g, p0, p1);
+          if (lane == 0) where[0] = g, where[1] = p0, where[2] = p1;
+        }
+        if (!together()) { ok = false; break; }
+        const int p0 = where[1], count = where[2] - p0;
+        if (threadIdx.x < TM) {
+          const int row = (int)threadIdx.x < count ? __ldcg(order + p0 + threadIdx.x) : -1;
+          rows[threadIdx.x] = (unsigned)row < (unsigned)T ? row : -1;
+        }
+        const float f = scale ? __ldcg(scale + where[0]) : 1.f;
+        for (int i = threadIdx.x; i < TM * (r16 / 4); i += WORK * 32) {
+          const int p = i / (r16 / 4), j = 4 * (i - p * (r16 / 4));
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p < count && j < r) {
+            const float *src = t + ((int64_t)v.s * T + p0 + p) * r + j;
+#pragma unroll 4
+            for (int z = 0; z < shares; ++z) {
+              const float4 w = __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)z * S * T * r));
+              a.x += w.x; a.y += w.y; a.z += w.z; a.w += w.w;
+            }
+          }
+          const float e[4] = {a.x * f, a.y * f, a.z * f, a.w * f};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            hi[x] = qld::f32_to_bf16_rn(e[x]);
+            const float rest = e[x] - qld::bf16_to_f32(hi[x]);
+            lo[x] = rest == rest ? qld::f32_to_bf16_rn(rest) : 0;   // inf and NaN are in hi alone
+          }
+          const uint32_t at = tb + (j >> 6) * TM * 128 + p * 128 + ((((j & 63) >> 3) ^ (p & 7)) << 4) + (j & 7) * 2;
+          sts64(at, hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          sts64(at + kch * TM * 128, lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        }
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(t_full);
+        if (!together()) { ok = false; break; }          // rows
+      }
+      // this lane's old outputs: features n .. n + 7 of two strips of 32, positions gid and gid + 8 of two 16s
+      const int n0 = v.c * TN + 64 * part + 8 * tig;
+      uint4 old[2][2][2][F32 ? 2 : 1];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = rows[32 * q + 16 * h + 8 * e + gid], n = n0 + 32 * cc;
+            if (row < 0 || n >= N) continue;
+            const uint4 *y = reinterpret_cast<const uint4 *>(static_cast<const char *>(L.y[v.s]) + ((size_t)row * N + n) * (F32 ? 4 : 2));
+#pragma unroll
+            for (int i = 0; i < (F32 ? 2 : 1); ++i) old[cc][h][e][i] = __ldcg(y + i);
+          }
+      if (!warp_wait(d_full + 8 * d, (k >> 1) & 1)) { ok = false; break; }
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[16];
+          tmem_ld_16x256b_x4(tmem + ((uint32_t)(32 * q + 16 * h) << 16) + d * TN + 64 * part + 32 * cc, w);
+          sm100::tmem_wait_ld();
+          const int n = n0 + 32 * cc;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = rows[32 * q + 16 * h + 8 * e + gid];
+            if (row < 0 || n >= N) continue;
+            float add[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              add[2 * j] = __uint_as_float(w[4 * j + 2 * e]);
+              add[2 * j + 1] = __uint_as_float(w[4 * j + 2 * e + 1]);
+            }
+            if constexpr (F32) {
+              float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(L.y[v.s]) + (size_t)row * N + n);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 o = old[cc][h][e][i];
+                y[i] = make_float4(__uint_as_float(o.x) + add[4 * i], __uint_as_float(o.y) + add[4 * i + 1],
+                                   __uint_as_float(o.z) + add[4 * i + 2], __uint_as_float(o.w) + add[4 * i + 3]);
+              }
+            } else {
+              const uint4 o = old[cc][h][e][0];
+              const uint32_t ou[4] = {o.x, o.y, o.z, o.w};
+              uint32_t x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[i] = pack2(qld::bf16_to_f32(ou[i] & 0xffffu) + add[2 * i],
+                             __uint_as_float(ou[i] & 0xffff0000u) + add[2 * i + 1], OUT_BF16);
+              *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(L.y[v.s]) + (size_t)row * N + n) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(d_free + 8 * d);
+    }
+  }
+  if (!ok) atomicExch(&g_lora_timeout, 1);
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == WORK) {
+    __syncwarp();
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, 512);
+  }
+}
+
+size_t smem_bytes(int r) { return (size_t)((r + 63) / 64) * (2 * TM + BST * TN) * 128 + 1024; }
+
+}  // namespace
+
+namespace lora {
+
+// Whole strips of 32 features (the copy's outermost dimension), 16-byte rows of B, ranks whose operands fit, and rows
+// enough that tiles of 128 positions fill: 48 per adapter on average.
+bool expand_mma_takes(const Layers &L, int S, int G, int T, int r) {
+  if (r % 8 || r > RMAX || T / std::min(G, T) < 48) return false;
+  for (int i = 0; i < S; ++i)
+    if (L.N[i] % 32 || (int64_t)G * L.N[i] / 32 >= ((int64_t)1 << 31)) return false;
+  return true;
+}
+
+ql_status expand_mma_launch(const Layers &in, int S, const int32_t *order, const int32_t *offsets, const float *scale,
+                            ql_out_dtype ydt, int G, int T, int r, int shares, const float *t, cudaStream_t s) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return ql::fail(QL_ERR_CUDA, "lora_add: cuTensorMapEncodeTiled is unavailable");
+  Maps maps{};
+  Layers L = in;
+  int64_t units = 0;
+  for (int i = 0; i < S; ++i) {
+    L.chunk0[i + 1] = L.chunk0[i] + (L.N[i] + TN - 1) / TN;
+    const cuuint64_t rowb = (cuuint64_t)r * 2;
+    const cuuint64_t dims[5] = {(cuuint64_t)r, 2, 4, 4, (cuuint64_t)G * L.N[i] / 32};
+    const cuuint64_t strides[4] = {rowb, 8 * rowb, 2 * rowb, 32 * rowb};
+    const cuuint32_t box[5] = {64, 2, 4, 4, TN / 32};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    if (enc(&maps.b[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint16_t *>(L.B[i]), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return ql::fail(QL_ERR_CUDA, "lora_add: cannot encode the tensor map of B");
+  }
+  units = ((int64_t)std::min(G, T) + T / TM) * L.chunk0[S];
+  const int grid = (int)std::min<int64_t>(units, ql::sm_count());
+  const size_t smem = smem_bytes(r);
+  auto go = [&](auto kern) -> ql_status {
+    if (ql::set_max_smem(kern, (int)smem) != cudaSuccess) return ql::fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
+    ql::launch(kern, grid, THREADS, smem, s, maps, L, S, order, offsets, scale, G, T, r, shares, t);
+    return ql::launch_status("lora_add (expand)");
+  };
+  return ydt == QL_OUT_F32 ? go(lora_expand_mma_kernel<true>) : go(lora_expand_mma_kernel<false>);
+}
+
+}  // namespace lora
+
+namespace ql {
+
+ql_status lora_read_timeout(int *flag) {
+  int zero = 0;
+  if (cudaMemcpyFromSymbol(flag, g_lora_timeout, sizeof(int)) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_lora_timeout, &zero, sizeof(int)) != cudaSuccess)
+    return fail(QL_ERR_CUDA, "ql_check: cannot read the device timeout flag");
+  return QL_OK;
+}
+
+}  // namespace ql

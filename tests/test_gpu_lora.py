@@ -52,6 +52,9 @@ CASES = [
     (16, 16, 16, 1024, (512,)), (33, 4, 64, 640, (257, 96, 1, 40)), (64, 2, 17, 1000, (320,)), (100, 40, 4, 192, (200,)),
     (257, 3, 32, 320, (264,)), (130, 1, 256, 512, (200,)), (600, 5, 64, 192, (136,)), (50, 3, 96, 5120, (1024,)),
     (9, 9, 130, 264, (72,)),
+    # many rows per adapter, features in whole strips of 32
+    (400, 3, 64, 192, (544, 96)), (300, 2, 24, 128, (288,)), (500, 4, 128, 256, (1056,)), (700, 1, 8, 64, (64, 32, 32, 96)),
+    (129, 1, 72, 72, (2080,)), (1000, 5, 40, 320, (512, 256)),
 ]
 
 

@@ -152,7 +152,7 @@ def test_binding_refuses_wrong_tensors(ql):
     with pytest.raises(ValueError, match="CUDA tensors"):
         ql.lora_add([(a, b, y)], x, rows, off)
     with pytest.raises(ValueError, match="x_div"):
-        ql._groups_c(G, off, x, y, None, 2, None)
+        ql._groups_c(G, off, x, y, None, 2, None, 0)
     with pytest.raises(ValueError, match="one entry"):
-        ql._groups_c(G, off, x, y, rows, 1, rows[:2])
+        ql._groups_c(G, off, x, y, rows, 1, rows[:2], 0)
     assert f32 is torch.float32 and ctypes.sizeof(ql.GroupsC) == 48

@@ -271,7 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ x producer
     const uint32_t lead_full = sm100::mapa_shared(bar.full_x, 0);
-    int st = 0, turn = 0;                      // steps of warp 0 and of warp 3 alternate
+    int st = 0;
+    const int b = warp & 1;                    // of each step, warp 0 copies the first K block and warp 3 the second
     uint32_t ph = 1;                           // a fresh barrier passes a wait for the phase before its first
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
       const Tile t = tile_at(wi);
@@ -292,45 +293,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
       for (int sp = 0; sp < nst; ++sp) {
-        if (turn == (warp & 1)) {
-          const int blocks = min(2, nkb - 2 * sp);
-          if (!warp_wait(bar.empty_x + 8 * st, ph, false)) { ok = false; break; }
-          if (lead && lane == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
-          __syncwarp();
-          const uint32_t dst = sbase + OFF_X + st * 2 * xblk, full = lead_full + 8 * st;
-          const int kx = 2 * sp * 64;
+        const int blocks = min(2, nkb - 2 * sp), kx = (2 * sp + b) * 64;
+        if (!warp_wait(bar.empty_x + 8 * st, ph, false)) { ok = false; break; }
+        if (b < blocks && sm100::elect_one()) {
+          const uint32_t dst = sbase + OFF_X + (2 * st + b) * xblk, full = lead_full + 8 * st;
+          if (lead && b == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
           if (a.g.x_rows) {
-            if (sm100::elect_one()) {
-              // four lists at a time are loaded before their copies are issued: a load's latency per copy, in the queue
-              // behind the lookups, made a gather take 40 clocks
-              const int n4 = t.halves * groups;
-              for (int i0 = 0; i0 < n4; i0 += 4) {
-                uint32_t r[4][4];
+            // four lists at a time are loaded before their copies are issued: a load's latency per copy, in the queue
+            // behind the lookups, made a gather take 40 clocks
+            const int n4 = t.halves * groups;
+            for (int i0 = 0; i0 < n4; i0 += 4) {
+              uint32_t r[4][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) lds128(list + 16 * (i0 + i), r[i][0], r[i][1], r[i][2], r[i][3]);
+              for (int i = 0; i < 4; ++i) lds128(list + 16 * (i0 + i), r[i][0], r[i][1], r[i][2], r[i][3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (i0 + i >= n4) break;
-                  const int4 y = make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]);
-                  const uint32_t to = dst + (i0 + i) * 512;
-                  sm100::tma_gather4_pair(to, &map_x, kx, y, full);
-                  if (blocks == 2) sm100::tma_gather4_pair(to + xblk, &map_x, kx + 64, y, full);
-                }
+              for (int i = 0; i < 4; ++i) {
+                if (i0 + i >= n4) break;
+                sm100::tma_gather4_pair(dst + (i0 + i) * 512, &map_x, kx,
+                                        make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]), full);
               }
             }
-            __syncwarp();
-          } else if (sm100::elect_one()) {      // rows past the tile are other rows, whose columns are not stored
+          } else {                               // rows past the tile are other rows, whose columns are not stored
             for (int h = 0; h < t.halves; ++h)
-              for (int j = 0; j < boxes; ++j) {
-                const uint32_t to = dst + (h * boxes + j) * X_BOX * 128;
-                const int y = t.p0 + h * t.nh + (int)rank * nr + j * X_BOX;
-                sm100::tma_load_2d_pair(to, &map_x, kx, y, full);
-                if (blocks == 2) sm100::tma_load_2d_pair(to + xblk, &map_x, kx + 64, y, full);
-              }
+              for (int j = 0; j < boxes; ++j)
+                sm100::tma_load_2d_pair(dst + (h * boxes + j) * X_BOX * 128, &map_x, kx,
+                                        t.p0 + h * t.nh + (int)rank * nr + j * X_BOX, full);
           }
-          __syncwarp();
         }
-        turn ^= 1;
+        __syncwarp();
         if (++st == a.xst) {
           st = 0;
           ph ^= 1;

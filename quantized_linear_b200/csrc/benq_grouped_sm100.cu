@@ -3,7 +3,7 @@
 //
 // The product is taken transposed: the MMA's M side is W (decoded), its N side the positions of one
 // group, so a group of c positions costs ceil(c / 16) * 16 columns and no padding to a 128-row tile.  The
-// work unit is a CTA pair (two SMs) and a tile of 2 x 128 rows of W by up to 384 positions.
+// work unit is a CTA pair (two SMs) and a tile of 2 x 128 rows of W by up to 256 positions.
 //
 // What bounds such a kernel is the shared-memory port (128 bytes per clock and SM): a table lookup moves 2
 // of the 4 bytes of each bank, the X tile is written once by TMA and read by the tensor core.  Hence:
@@ -15,20 +15,24 @@
 // Per 64-wide K block and SM that is 256 + 48 wavefronts of lookups and codes, 48 of code writes and
 // n/2 + n/2 of X for n positions, against 2 n clocks of MMA.
 //
-// Roles (768 threads per CTA): warps 0 and 3 load X on alternate steps (rows gathered by x_rows, or tiles); warp 1
-// issues the MMAs (even CTA); warp 2 loads codes and, between them, lays out the next tile's tables; warps 4-7 drain
-// the accumulators; warps 8-23, four warpgroups, decode: two to a step of two K blocks, in turn, because a warp's
-// waits and hand-over take as long as its lookups (two warpgroups left the port idle half of the time).  Accumulators are two
-// slots of 192 columns, so one tile's epilogue overlaps the next tile's MMAs.  The decoders of the odd CTA arrive at
-// the even CTA's barrier with relaxed semantics: what they hand over is in tensor memory, which the tcgen05 fences
-// order (a cluster-scope release by one relaying thread took 1300 clocks per K block and set the kernel's pace).
+// Roles (896 threads per CTA), in steps of two K blocks: warps 0, 3 and 24-27 load X, half of them each K block (rows
+// gathered by x_rows, four to a copy that takes 50 clocks to issue, or tiles); warp 1 issues the MMAs (even CTA);
+// warp 2 loads codes and, between them, lays out the next tile's tables; warps 4-7 drain the accumulators; warps 8-23
+// are four warpgroups of decoders, each taking every fourth step.  Accumulators are two slots, so that one tile's
+// epilogue overlaps the next tile's MMAs.  The decoders of the odd CTA arrive at the even CTA's barrier with relaxed
+// semantics: what they hand over is in tensor memory, which the tcgen05 fences order (a cluster-scope release by one
+// relaying thread took 1300 clocks per K block and set the kernel's pace).
+//
+// Measured for a K block of 2 x 128 rows: lookups alone 311 clocks (16 warps, with the stores to tensor memory); the
+// kernel takes about 580 with few positions, where the decoders' waits and the polling of the other warps share the
+// issue slots with the lookups, and about 950 with 256 gathered positions.
 //
 // The gated form gives each warp of lanes 16 gate rows and the same features' 16 up rows: silu(g) * u then needs
 // one exchange between the halves of a warp.
 //
 // The tensor core adds to its fp32 accumulator with truncation, about K * 1e-9 of the result after K
-// inputs.  That is far below a bf16 rounding; for fp32 outputs each run of `seg` K blocks (512 inputs, more only
-// above K = 12288) goes to an accumulator of its own and the epilogue adds the runs in fp32.
+// inputs.  That is far below a bf16 rounding; for fp32 outputs each run of `seg` steps (512 inputs, more only
+// above K = 8192) goes to an accumulator of its own and the epilogue adds the runs in fp32.
 #include <cuda.h>
 
 #include <algorithm>
@@ -44,9 +48,9 @@ namespace {
 using namespace pairgemm;
 
 constexpr int RW = 128;                        // rows of W per CTA and tile
-constexpr int NS = 192;                        // positions per accumulator slot (the MMA's N)
-constexpr int NT = 2 * NS;                     // positions per tile at most
-constexpr int SA = 2, SC = 3;                  // stages: decoded W (steps), codes
+constexpr int NT = 256;                        // positions per tile at most (two MMAs of half as many, N)
+constexpr int SA_MAX = 6, SC = 3;              // stages: decoded W (steps, as many as tensor memory has room for, at
+                                               // least one per decoder warpgroup), codes
 constexpr int X_RING = 96 * 1024;              // x stages of one step each: two 64-column blocks of half a tile's rows
 constexpr int SX_MAX = 8;
 constexpr int X_BOX = 32;                      // rows per copy when rows are not gathered
@@ -54,29 +58,32 @@ constexpr int C_LINE = 128;                    // code bytes per row and stage: 
 constexpr int C_BYTES = RW * C_LINE;           // 144-byte rows, three K blocks, took the TMA unit 21 clocks each.)  16 KB
 constexpr int TBL_BYTES = 4 * 8192;            // lane-private tables: 4 warps of rows x [64][32] words, two buffers
 constexpr int NDW = 16;                        // decoder warps: four warpgroups, two per step in turn
-constexpr int THREADS = (8 + NDW) * 32;
-constexpr int D_COL = 0, A_COL = NT;           // tensor memory columns: accumulators, then SA steps of 2 x 32
-constexpr int MAX_SEG = NT / 16;               // runs of K blocks with an accumulator each (fp32 outputs)
+constexpr int XPARTS = 3;                      // warps that copy a K block's x rows
+constexpr int THREADS = (8 + NDW + 2 * (XPARTS - 1)) * 32;
+constexpr int D_MAX = 256;                     // tensor memory columns: at most these are accumulators, then steps of 2 x 32
+constexpr int MAX_SEG = D_MAX / 16;            // runs of K blocks with an accumulator each (fp32 outputs)
 constexpr int SEG_STEPS = 4;                   // 512 inputs
 // Shared memory: barriers and the tile counts in front of the tables, which start on 8 KB (a lookup ORs the code into
 // the address).  The front's size puts them there when dynamic shared memory starts at 1 KB, as it does after the
 // kilobyte that the system keeps; the kernel checks it.
 constexpr int FRONT = 8192 - 1024;
-constexpr int NBAR = 2 * SX_MAX + 2 * SA + 2 * SC + 8;
+constexpr int NBAR = 2 * SX_MAX + 2 * SA_MAX + 2 * SC + 8;
 constexpr int OFF_MISC = NBAR * 8;             // tensor-memory address, abort flag
 constexpr int OFF_GRP = OFF_MISC + 16;         // token tiles before each group, int [G + 1]
 constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
 constexpr int OFF_C = OFF_X + X_RING;
 constexpr int STG_BYTES = 1024;                // per epilogue warp: 16 positions x 32 features of bf16
 constexpr int OFF_STG = OFF_C + SC * C_BYTES;
-constexpr int OFF_ROW = OFF_STG + 4 * STG_BYTES;      // per x warp: the gathered rows of its tile, int [NS]
-constexpr int OFF_YROW = OFF_ROW + 2 * NS * 4;        // per epilogue warp: the output rows of a slot, int [NS]
-constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * NS * 4;
+constexpr int OFF_ROW = OFF_STG + 4 * STG_BYTES;      // per x warp: the gathered rows of its part, int [XLIST]
+constexpr int XLIST = (NT / 2 / 4 + XPARTS - 1) / XPARTS * 4;   // rows of a part, at most
+constexpr int OFF_YROW = OFF_ROW + 2 * XPARTS * XLIST * 4;        // per epilogue warp: the output rows of a slot, int [NT / 2]
+constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * (NT / 2) * 4;
 static_assert(OFF_GRP + (QL_MAX_GROUPS + 1) * 4 <= FRONT, "front");
-static_assert(A_COL + 64 * SA <= 512, "tensor memory");
+static_assert(D_MAX + 64 * 4 <= 512, "tensor memory: four stages of decoded W beside the accumulators");
 static_assert(OFF_X % 1024 == 0 && OFF_C % 128 == 0 && C_BYTES % 1024 == 0 && OFF_C % 1024 == 0 && OFF_STG % 128 == 0, "alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr uint16_t PAIR = 0x3;
+constexpr unsigned NAP = 32, LONG_NAP = 128;   // ns between tries of warps that run ahead, and of the epilogue
 
 __device__ int g_grouped_timeout = 0;
 
@@ -85,8 +92,8 @@ struct Bars {
   // CTA; empty_x, empty_a: its MMAs are done, in both.
   uint32_t full_x, empty_x, ready_a, empty_a, full_c, empty_c, tbl_full, tbl_empty, acc_full, acc_empty;
   __device__ Bars(uint32_t b)
-      : full_x(b), empty_x(full_x + 8 * SX_MAX), ready_a(empty_x + 8 * SX_MAX), empty_a(ready_a + 8 * SA),
-        full_c(empty_a + 8 * SA), empty_c(full_c + 8 * SC), tbl_full(empty_c + 8 * SC), tbl_empty(tbl_full + 8 * 2),
+      : full_x(b), empty_x(full_x + 8 * SX_MAX), ready_a(empty_x + 8 * SX_MAX), empty_a(ready_a + 8 * SA_MAX),
+        full_c(empty_a + 8 * SA_MAX), empty_c(full_c + 8 * SC), tbl_full(empty_c + 8 * SC), tbl_empty(tbl_full + 8 * 2),
         acc_full(tbl_empty + 8 * 2), acc_empty(acc_full + 8 * 2) {}
 };
 
@@ -96,6 +103,7 @@ struct Args {
   void *y;
   int ydt, N, K, ntl, nt_max;   // tiles of W rows per group, positions per tile at most
   int xr, xst;                       // rows per 64-column block of an x stage, x stages
+  int slot, sa;                      // columns of each of the two accumulator slots, stages of decoded W behind them
   int vec;                           // bf16 rows of whole 16-byte pieces
   int seg, nseg;                     // steps per run of its own accumulator, runs
 };
@@ -138,7 +146,7 @@ struct Lookup {
   static __device__ __forceinline__ void run(const uint32_t (&w)[12], uint32_t base, uint32_t (&out)[32]) {
     Lookup<J - 2>::run(w, base, out);
     const uint32_t a = lds32(entry_at<J - 2>(w, base)), b = lds32(entry_at<J - 1>(w, base));
-    out[(J - 2) / 2] = __byte_perm(a, b, 0x5410);
+    asm("mad.lo.u32 %0, %1, 65536, %2;" : "=r"(out[(J - 2) / 2]) : "r"(b), "r"(a));   // b << 16 | a, off the ALU pipe
   }
 };
 template <>
@@ -161,6 +169,48 @@ __device__ __forceinline__ void store_out(void *y, int ydt, size_t i, float v) {
     static_cast<uint16_t *>(y)[i] = qld::f32_to_bf16_rn(v);
 }
 
+// Up to eight tries of a wait, four instructions each.  A try is suspended while nothing happens on the SM's barriers, but
+// on a busy SM it returns every 200 clocks or so, and with a clock and a flag looked at each time two dozen waiting warps
+// took 40 % of the issue slots from the decoders.
+__device__ __forceinline__ bool try_wait8(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra D;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "D: selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The bounded wait of this kernel (as pairgemm::Waiter): gives up when the budget runs out or the pair's abort flag is
+// set, and then sets it in both CTAs.  nap: nanoseconds between rounds of tries, for warps that run ahead of the others.
+struct Wait {
+  uint32_t abort_local, abort_peer;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, unsigned nap) const {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+      if (nap) __nanosleep(nap);
+      if (try_wait8(bar, parity)) return true;
+      if (ld_volatile_u32(abort_local) != 0) return false;
+      if (clock64() - t0 > WAIT_BUDGET) {
+        sts32(abort_local, 1);
+        st_cluster_u32(abort_peer, 1);
+        return false;
+      }
+    }
+  }
+};
+
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     benq_grouped_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
@@ -180,15 +230,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int G = a.g.G;
   const uint32_t rank = sm100::cluster_ctarank();
   const bool lead = rank == 0;
-  const Waiter wt{tmem_slot + 4, sm100::mapa_shared(tmem_slot + 4, rank ^ 1u)};
+  const Wait wt{tmem_slot + 4, sm100::mapa_shared(tmem_slot + 4, rank ^ 1u)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int nkb = a.K / 64, nst = (nkb + 1) / 2;   // K blocks, steps
   const uint32_t xblk = a.xr * 128;                // bytes of a 64-column block of an x stage
   bool ok = true;
   // a wait of a whole warp: no lane goes on alone when one gave up
-  auto warp_wait = [&](uint32_t b, uint32_t parity, bool cluster_scope) {
-    return __all_sync(0xffffffffu, wt.wait(b, parity, cluster_scope)) != 0;
+  auto warp_wait = [&](uint32_t b, uint32_t parity, unsigned nap) {
+    return __all_sync(0xffffffffu, wt(b, parity, nap)) != 0;
   };
 
   if (threadIdx.x == 0) {
@@ -196,13 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       sm100::mbar_init(bar.full_x + 8 * s, 1);
       sm100::mbar_init(bar.empty_x + 8 * s, 1);
     }
-    for (int s = 0; s < SA; ++s) {
-      sm100::mbar_init(bar.ready_a + 8 * s, NDW);       // half of the decoder warps of both CTAs
+    for (int s = 0; s < SA_MAX; ++s) {
+      sm100::mbar_init(bar.ready_a + 8 * s, 2 * 4);     // a decoder warpgroup of each CTA
       sm100::mbar_init(bar.empty_a + 8 * s, 1);
     }
     for (int s = 0; s < SC; ++s) {
       sm100::mbar_init(bar.full_c + 8 * s, 1);
-      sm100::mbar_init(bar.empty_c + 8 * s, 4 * 4);     // four K blocks' warps
+      sm100::mbar_init(bar.empty_c + 8 * s, 2 * 4);     // two steps' warps
     }
     for (int s = 0; s < 2; ++s) {
       sm100::mbar_init(bar.tbl_full + 8 * s, 1);
@@ -247,6 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   sm100::cluster_sync();   // both CTAs' barriers initialised, tensor memory allocated, tiles counted
   sm100::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_raw + OFF_MISC);
+  const uint32_t a_col = tmem + 2 * a.slot;        // the stages of decoded W
   const int nitems = cum[G] * a.ntl;
   auto tile_at = [&](int item) {
     Tile t;
@@ -263,61 +314,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     t.p0 = s0 + (tt - cum[lo]) * per;
     t.p1 = min(s1, t.p0 + per);
     const int n = (per + 15) & ~15;
-    t.halves = n > NS ? 2 : 1;
+    t.halves = n > a.slot ? 2 : 1;
     t.nh = t.halves == 2 ? ((n / 2 + 15) & ~15) : n;
     return t;
   };
 
-  if (warp == 0 || warp == 3) {
+  if (warp == 0 || warp == 3 || warp >= 8 + NDW) {
     // ------------------------------------------------------------ x producer
     const uint32_t lead_full = sm100::mapa_shared(bar.full_x, 0);
     int st = 0;
-    const int b = warp & 1;                    // of each step, warp 0 copies the first K block and warp 3 the second
+    // of each step, half of the x warps copy the first K block and half the second, each a part of its rows
+    const int xi = warp == 0 ? 0 : warp == 3 ? 1 : warp - (8 + NDW) + 2, b = xi & 1, part = xi >> 1;
     uint32_t ph = 1;                           // a fresh barrier passes a wait for the phase before its first
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
       const Tile t = tile_at(wi);
       const int nr = t.nh / 2;                 // rows of this CTA per half
-      const int groups = nr / 4, boxes = (nr + X_BOX - 1) / X_BOX;
+      const int boxes = (nr + X_BOX - 1) / X_BOX;
       const int rows = a.g.x_rows ? nr : boxes * X_BOX;   // rows copied per half
-      // gathered rows: both halves' lists one after the other; a place past the tile or a row out of range reads row
-      // 0, whose column is not stored
-      const uint32_t list = sbase + OFF_ROW + (warp & 1) * NS * 4;
+      // gathered rows, both halves' one after the other, in groups of four, of which this warp has g0 .. g1 - 1: a place
+      // past the tile or a row out of range reads row 0, whose column is not stored
+      const uint32_t list = sbase + OFF_ROW + xi * XLIST * 4;
+      const int groups = t.halves * nr / 4, g0 = groups * part / XPARTS, g1 = groups * (part + 1) / XPARTS;
       if (a.g.x_rows) {
         __syncwarp();
-        for (int i = lane; i < t.halves * nr; i += 32) {
+        for (int i = 4 * g0 + lane; i < 4 * g1; i += 32) {
           const int h = i >= nr, p = t.p0 + h * t.nh + (int)rank * nr + i - (h ? nr : 0);
           int x = 0;
           if (p < t.p1) x = __ldcg(a.g.x_rows + p) / a.g.x_div;
-          sts32(list + 4 * i, (unsigned)x < (unsigned)a.g.X ? x : 0);
+          sts32(list + 4 * (i - 4 * g0), (unsigned)x < (unsigned)a.g.X ? x : 0);
         }
         __syncwarp();
       }
       for (int sp = 0; sp < nst; ++sp) {
         const int blocks = min(2, nkb - 2 * sp), kx = (2 * sp + b) * 64;
-        if (!warp_wait(bar.empty_x + 8 * st, ph, false)) { ok = false; break; }
+        if (!warp_wait(bar.empty_x + 8 * st, ph, NAP)) { ok = false; break; }
         if (b < blocks && sm100::elect_one()) {
           const uint32_t dst = sbase + OFF_X + (2 * st + b) * xblk, full = lead_full + 8 * st;
-          if (lead && b == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
+          if (lead && xi == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
           if (a.g.x_rows) {
-            // four lists at a time are loaded before their copies are issued: a load's latency per copy, in the queue
-            // behind the lookups, made a gather take 40 clocks
-            const int n4 = t.halves * groups;
-            for (int i0 = 0; i0 < n4; i0 += 4) {
-              uint32_t r[4][4];
+            // the next four lists are loaded while four copies are issued (50 clocks each)
+            uint32_t r[4][4];
+            auto load = [&](int i0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) lds128(list + 16 * (i0 + i), r[i][0], r[i][1], r[i][2], r[i][3]);
+              for (int i = 0; i < 4; ++i)
+                if (i0 + i < g1) lds128(list + 16 * (i0 + i - g0), r[i][0], r[i][1], r[i][2], r[i][3]);
+            };
+            load(g0);
+            for (int i0 = g0; i0 < g1; i0 += 4) {
+              int4 y[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (i0 + i >= n4) break;
-                sm100::tma_gather4_pair(dst + (i0 + i) * 512, &map_x, kx,
-                                        make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]), full);
-              }
+              for (int i = 0; i < 4; ++i) y[i] = make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]);
+              load(i0 + 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i0 + i < g1) sm100::tma_gather4_pair(dst + (i0 + i) * 512, &map_x, kx, y[i], full);
             }
           } else {                               // rows past the tile are other rows, whose columns are not stored
-            for (int h = 0; h < t.halves; ++h)
-              for (int j = 0; j < boxes; ++j)
-                sm100::tma_load_2d_pair(dst + (h * boxes + j) * X_BOX * 128, &map_x, kx,
-                                        t.p0 + h * t.nh + (int)rank * nr + j * X_BOX, full);
+            for (int j = part; j < t.halves * boxes; j += XPARTS) {
+              const int h = j >= boxes;
+              sm100::tma_load_2d_pair(dst + j * X_BOX * 128, &map_x, kx,
+                                      t.p0 + h * t.nh + (int)rank * nr + (j - (h ? boxes : 0)) * X_BOX, full);
+            }
           }
         }
         __syncwarp();
@@ -339,8 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int slots = a.nseg > 1 ? 2 : t.halves, first_slot = sl.take(slots);
         // a tile of two slots waits for the second one when its first step has multiplied into the first
         const bool wait1 = first_slot + slots == 2 && sl.used1 > 0, late1 = t.halves == 2;
-        if ((first_slot == 0 && sl.used0 > 0 && !warp_wait(bar.acc_empty, (sl.used0 - 1) & 1, true)) ||
-            (wait1 && !late1 && !warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, true))) {
+        if ((first_slot == 0 && sl.used0 > 0 && !warp_wait(bar.acc_empty, (sl.used0 - 1) & 1, 0)) ||
+            (wait1 && !late1 && !warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, 0))) {
           ok = false;
           break;
         }
@@ -348,14 +405,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t idesc = sm100::idesc_bf16_f32(256, t.nh);
         // the second half's x rows follow the first's (whole copies when they are not gathered)
         const uint32_t half = (a.g.x_rows ? t.nh / 2 : (t.nh / 2 + X_BOX - 1) / X_BOX * X_BOX) * 128 >> 4;
-        uint32_t d0 = tmem + D_COL + first_slot * NS;
+        uint32_t d0 = tmem + first_slot * a.slot;
         int left = a.seg;                      // steps left in this run
         uint32_t add = 0;                      // 0 for the first MMA of a run, which overwrites
         for (int sp = 0; sp < nst; ++sp) {
-          if (!warp_wait(bar.full_x + 8 * sx, phx, false) || !warp_wait(bar.ready_a + 8 * sa, pha, false)) { ok = false; break; }
+          if (!warp_wait(bar.full_x + 8 * sx, phx, 0) || !warp_wait(bar.ready_a + 8 * sa, pha, 0)) { ok = false; break; }
           sm100::tc_fence_after();
           const int blocks = min(2, nkb - 2 * sp);
-          const uint32_t at0 = tmem + A_COL + sa * 64;
+          const uint32_t at0 = a_col + sa * 64;
           const uint64_t bd0 = xdesc + (sx * 2 * xblk >> 4);
           auto mmas = [&](uint32_t d, uint64_t bd) {
 #pragma unroll
@@ -370,10 +427,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (t.halves == 2) {
             if (sp == 0 && wait1) {
-              if (!warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, true)) { ok = false; break; }
+              if (!warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, 0)) { ok = false; break; }
               sm100::tc_fence_after();
             }
-            if (sm100::elect_one()) mmas(d0 + NS, bd0 + half);
+            if (sm100::elect_one()) mmas(d0 + a.slot, bd0 + half);
             __syncwarp();
           }
           if (sm100::elect_one()) {
@@ -391,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             sx = 0;
             phx ^= 1;
           }
-          if (++sa == SA) {
+          if (++sa == a.sa) {
             sa = 0;
             pha ^= 1;
           }
@@ -455,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         load();
       }
       for (int ln = 0; ln < nln; ++ln) {
-        if (!warp_wait(bar.empty_c + 8 * sc, phc, false)) { ok = false; break; }
+        if (!warp_wait(bar.empty_c + 8 * sc, phc, NAP)) { ok = false; break; }
         if (sm100::elect_one()) {
           if (n0 < a.N) {
             const uint32_t dst = sbase + OFF_C + sc * C_BYTES;
@@ -473,70 +530,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         // Past SC stages the decoders are on this tile, so the buffer of the one before is free.
         if (q < 4 && ln >= SC) {
-          if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, false)) { ok = false; break; }
+          if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, NAP)) { ok = false; break; }
           store(b);
         }
       }
       if (ok && q < 4) {
-        if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, false)) ok = false;
+        if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, NAP)) ok = false;
         while (ok && q < 4) store(b);
       }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ decoders
+    // Warpgroup wg takes every fourth step, both of its K blocks.  A row's codes are a stream of 16-byte chunks, eight to
+    // a line (stage), six to a step: four steps are three lines, so that within a tile a warpgroup always finds its
+    // chunks in the same places of the same stages, a phase further each time.
     const int q = warp & 3, wg = (warp >> 2) - 2;
     // the row of the staged codes that this lane decodes
     const int row = GATED ? (lane < 16 ? 0 : RW / 2) + 16 * q + (lane & 15) : 32 * q + lane;
     const uint32_t crow = sbase + OFF_C + row * C_LINE;
-    const int sa = wg >> 1;                    // the stage of decoded W that this warpgroup writes, one of its two K blocks
-    const uint32_t ready = sm100::mapa_shared(bar.ready_a + 8 * sa, 0);
-    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + A_COL + sa * 64 + (wg & 1) * 32;
+    const uint32_t ready = sm100::mapa_shared(bar.ready_a, 0);
+    const uint32_t to = a_col + ((uint32_t)(32 * q) << 16);
     const int nln = (3 * nkb + 7) / 8;
-    int tl = 0;
+    int tl = 0, sa = wg;                       // this warpgroup's next stage of decoded W
+    uint32_t pha = 1;
     uint32_t line0 = 0, step0 = 0;             // lines and steps of the tiles before
     for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl, line0 += nln, step0 += nst) {
       const uint32_t tbl = sbase + (tl & 1) * TBL_BYTES + q * 8192 + lane * 4;
-      if (!warp_wait(bar.tbl_full + 8 * (tl & 1), (tl >> 1) & 1, false)) { ok = false; break; }
-      for (int sp = (int)((sa ^ step0) & 1); sp < nst; sp += 2) {
-        const int kb = 2 * sp + (wg & 1);
-        const bool live = kb < nkb;
-        uint32_t out[32];
-        if (live) {
-          // A row's codes are a stream of 16-byte chunks, eight to a line (stage): these are chunks 3 kb .. 3 kb + 2
-          const int l0 = 3 * kb >> 3, l1 = (3 * kb + 2) >> 3;
-          const uint32_t g0 = line0 + l0, g1 = line0 + l1;
-          const uint32_t s0 = g0 % SC, s1 = g1 % SC;
-          if (!warp_wait(bar.full_c + 8 * s0, (g0 / SC) & 1, false)) ok = false;
-          if (ok && l1 != l0 && !warp_wait(bar.full_c + 8 * s1, (g1 / SC) & 1, false)) ok = false;
-          if (!ok) break;
-          uint32_t w[12];
+      if (!warp_wait(bar.tbl_full + 8 * (tl & 1), (tl >> 1) & 1, 0)) { ok = false; break; }
+      int sp = (int)((wg - step0) & 3);
+      const int f = sp;                        // first own step: sp % 4 for all of them
+      const uint32_t g0 = line0 + (6 * f >> 3), g1 = g0 + 1;
+      const uint32_t s0 = g0 % SC, s1 = g1 % SC;
+      uint32_t ph0 = (g0 / SC) & 1, ph1 = (g1 / SC) & 1;
+      const bool two = f == 1 || f == 2;       // the step's chunks end in the next line
+      uint32_t at[6];
 #pragma unroll
-          for (int j = 0; j < 3; ++j) {
-            const int c = 3 * kb + j;
-            lds128(crow + ((c >> 3) == l0 ? s0 : s1) * C_BYTES + (((c ^ row) & 7) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2],
-                   w[4 * j + 3]);
+      for (int j = 0; j < 6; ++j) {
+        const int c = 6 * f + j;
+        at[j] = crow + ((c >> 3) == (6 * f >> 3) ? s0 : s1) * C_BYTES + (((c ^ row) & 7) << 4);
+      }
+      for (; sp < nst; sp += 4) {
+        const bool half = 2 * sp + 1 == nkb, last = sp + 1 == nst;   // half: a last step of one K block
+        const bool next = two && !(half && f == 2);
+        if (!warp_wait(bar.full_c + 8 * s0, ph0, 0) || (next && !warp_wait(bar.full_c + 8 * s1, ph1, 0))) { ok = false; break; }
+        ph0 ^= 1;
+        ph1 ^= 1;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          if (b == 1 && half) break;
+          uint32_t w[12], out[32];
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            lds128(b ? at[3 + j] : at[j], w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          if (b == 1 || half) {
+            // The codes are in registers (the arrival is ordered after the warp's loads): the lines go back before the
+            // lookups.  A line belongs to two steps, or to the tile's last one alone, which then arrives twice.
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_n(bar.empty_c + 8 * s0, last && f == 0 ? 2 : 1);
+              if (next) mbar_arrive_n(bar.empty_c + 8 * s1, last ? 2 : 1);
+            }
           }
           Lookup<64>::run(w, tbl, out);
-          __syncwarp();
-          if (lane == 0) {
-            // a line is given back by its three or four K blocks; its last one arrives for those that it lacks
-            auto give = [&](int l, uint32_t s) {
-              const bool last = kb == min(nkb - 1, (8 * l + 7) / 3);
-              mbar_arrive_n(bar.empty_c + 8 * s, last ? 4 - (kb - 8 * l / 3) : 1);
-            };
-            give(l0, s0);
-            if (l1 != l0) give(l1, s1);
+          if (b == 0) {
+            if (!warp_wait(bar.empty_a + 8 * sa, pha, 0)) { ok = false; break; }
+            sm100::tc_fence_after();
           }
+          sm100::tmem_st_32x32b_x32(to + sa * 64 + b * 32, out);
         }
-        if (!warp_wait(bar.empty_a + 8 * sa, (((step0 + sp) >> 1) & 1) ^ 1, false)) { ok = false; break; }
-        if (live) {
-          sm100::tc_fence_after();
-          sm100::tmem_st_32x32b_x32(to, out);
-          sm100::tmem_wait_st();
-          sm100::tc_fence_before();
-          __syncwarp();
+        if (!ok) break;
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive_cluster_relaxed(ready + 8 * sa);
+        sa += 4;                               // four steps on (a.sa >= 4)
+        if (sa >= a.sa) {
+          sa -= a.sa;
+          pha ^= 1;
         }
-        if (lane == 0) sm100::mbar_arrive_cluster_relaxed(ready);
       }
       if (!ok) break;
       __syncwarp();
@@ -557,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int h = 0; h < t.halves && ok; ++h) {
       const int es = first_slot + h, pbase = t.p0 + h * t.nh;
       // the output rows of the slot's positions, -1 for none: read while the products run
-      const uint32_t ylist = sbase + OFF_YROW + q * NS * 4;
+      const uint32_t ylist = sbase + OFF_YROW + q * (NT / 2) * 4;
       __syncwarp();
       for (int i = lane; i < t.nh; i += 32) {
         const int p = pbase + i;
@@ -570,13 +641,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         sts32(ylist + 4 * i, (uint32_t)yr);
       }
       __syncwarp();
-      if (!warp_wait(bar.acc_full + 8 * es, (es ? used1 : used0) & 1, true) ||
-          (runs && !warp_wait(bar.acc_full + 8, used1 & 1, true))) {
+      if (!warp_wait(bar.acc_full + 8 * es, (es ? used1 : used0) & 1, LONG_NAP) ||
+          (runs && !warp_wait(bar.acc_full + 8, used1 & 1, LONG_NAP))) {
         ok = false;
         break;
       }
       sm100::tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + D_COL + (runs ? 0 : es * NS);
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (runs ? 0 : es * a.slot);
       if (a.vec) {
         // bf16 rows of 8-feature pieces: fragments of 16 lanes (features) x 16 columns (positions), transposed on
         // their way through this warp's own kilobyte of shared memory, leave as 16-byte stores.  One store and a
@@ -729,18 +800,24 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
   CUtensorMap mc, mc2;
   if (!codes_map(&mc, codes) || !codes_map(&mc2, codes2 ? codes2 : codes))
     return fail(QL_ERR_CUDA, "%s: cannot encode the code tensor map", who);
-  Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), 0, 0, 0, ydt == QL_OUT_BF16 && N % 8 == 0, K, 1};
+  Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), 0, 0, 0, 0, 0, ydt == QL_OUT_BF16 && N % 8 == 0, K, 1};
   // Positions per tile: room for a group of four times the average length, so that few groups take a second pass
-  // over their codes, and no more than that, because shorter x stages are more of them.
-  const int want = std::max(1, (int)std::min<int64_t>(4LL * (g.M / g.G), NT));
-  auto room = [](int n) { return n <= NS ? (n + 63) / 64 * 64 : (n + 127) / 128 * 128; };   // 64, 128, 192, 256, 384
-  a.nt_max = room(want);
+  // over their codes, and no more than that: what accumulators and x rows do not take is more stages.  (4096 tokens of
+  // a 64-expert layer, 512 rows per expert: gate/up 1.26 ms with 128, 0.95 with 256; 256 tokens: 0.276 with 64, 0.239
+  // with 128.)
+  auto room = [](int n) { return n <= 64 ? 64 : n <= 128 ? 128 : 256; };
+  a.nt_max = room((int)std::min<int64_t>(4LL * (g.M / g.G), NT));
   const int steps = (K / 64 + 1) / 2;
   if (ydt == QL_OUT_F32 && steps > SEG_STEPS) {
     a.seg = std::max(SEG_STEPS, (steps + MAX_SEG - 1) / MAX_SEG);
     a.nseg = (steps + a.seg - 1) / a.seg;
-    a.nt_max = std::min({a.nt_max, NS, NT / a.nseg / 16 * 16});   // every run's accumulator fits beside the others
+    a.nt_max = std::min({a.nt_max, 128, D_MAX / a.nseg / 16 * 16});   // every run's accumulator fits beside the others
   }
+  // a tile of up to 128 positions takes one slot, a longer one both; runs share them
+  a.slot = a.nseg > 1 ? (a.nseg * a.nt_max / 2 + 15) / 16 * 16 : std::min(a.nt_max, 128);
+  // A warpgroup comes back to a stage after four steps: with four stages or more its last wait has shown that all but
+  // one of the stage's earlier uses are over, so the phase's parity tells the one that it waits for.
+  a.sa = std::min(SA_MAX, (512 - 2 * a.slot) / 64);
   a.xr = room(a.nt_max) / 2;
   a.xst = std::min(SX_MAX, X_RING / (2 * a.xr * 128));
   // the most tiles that the counts could make (each group may end inside a tile)

@@ -473,7 +473,7 @@ ql_status ql_check(ql_stream_t stream) {
   g_msg[0] = 0;
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(QL_ERR_CUDA, "ql_check: %s", cudaGetErrorString(e));
-  int flag = 0, flag2 = 0, flag3 = 0, flag4 = 0, flag5 = 0;
+  int flag = 0, flag2 = 0, flag3 = 0, flag4 = 0, flag5 = 0, flag6 = 0;
   ql_status st = ql::benq_gemm_read_timeout(&flag);
   if (st != QL_OK) return st;
   st = ql::mdbf_read_timeout(&flag2);
@@ -484,11 +484,14 @@ ql_status ql_check(ql_stream_t stream) {
   if (st != QL_OK) return st;
   st = ql::lora_read_timeout(&flag5);
   if (st != QL_OK) return st;
+  st = ql::moe_combine_read_timeout(&flag6);
+  if (st != QL_OK) return st;
   if (flag) return fail(QL_ERR_TIMEOUT, "a bounded device-side wait of the GEMM ran out (code %d)", flag);
   if (flag2) return fail(QL_ERR_TIMEOUT, "a bounded device-side wait of the MDBF F stage ran out (code %d)", flag2);
   if (flag3) return fail(QL_ERR_TIMEOUT, "a bounded device-side wait of the MDBF GEMM ran out (code %d)", flag3);
   if (flag4) return fail(QL_ERR_TIMEOUT, "a bounded device-side wait of the grouped products ran out (code %d)", flag4);
   if (flag5) return fail(QL_ERR_TIMEOUT, "a bounded device-side wait of lora_add ran out (code %d)", flag5);
+  if (flag6) return fail(QL_ERR_TIMEOUT, "a bounded device-side wait of moe_combine ran out (code %d)", flag6);
   return QL_OK;
 }
 

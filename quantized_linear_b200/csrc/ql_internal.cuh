@@ -90,7 +90,8 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
                                   const ql_groups &g, const uint16_t *x, void *y, ql_out_dtype ydt, int N, int K,
                                   cudaStream_t s);
 ql_status benq_grouped_read_timeout(int *flag);   // reads and clears the grouped kernel's bounded-wait flag
-ql_status lora_read_timeout(int *flag);
+ql_status lora_read_timeout(int *flag);          // and the same of lora_add and moe_combine
+ql_status moe_combine_read_timeout(int *flag);
 size_t lora_workspace_size(int S, int T, int r);
 ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order,
                           const int32_t *offsets, const float *scale, ql_out_dtype ydt, int G, int T, int r, int K,

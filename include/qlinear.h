@@ -330,7 +330,7 @@ typedef struct {
   const int32_t *x_rows;  /* [M] or NULL: position i reads row x_rows[i] / x_div of x (NULL: row i) */
   const int32_t *y_rows;  /* [M] or NULL: position i writes row y_rows[i] of y (NULL: row i); no row twice */
   int x_div;              /* >= 1; x_rows holds slots t * k + j of a token t, with x_div = k, or rows with 1 */
-  int G, M;               /* groups (1 .. QL_MAX_GROUPS), positions (>= 0) */
+  int G, M;               /* groups (1 .. QL_MAX_GROUPS), positions (0 .. QL_MAX_POSITIONS) */
   int X, Y;               /* rows of x and of y; positions outside them are skipped */
 } ql_groups;
 
@@ -342,7 +342,8 @@ typedef struct {
  *   offsets  device int32 [G + 1], written.
  *   workspace device, 256-byte aligned, at least group_rows_workspace_bytes(M, G) bytes (NULL with 0
  *            when that is 0); contents need no clearing; not shared with a concurrent call.
- *   0 <= M <= QL_MAX_POSITIONS (QL_ERR_UNSUPPORTED above), 1 <= G <= QL_MAX_GROUPS.  The result depends on nothing but index.
+ *   0 <= M <= QL_MAX_POSITIONS (QL_ERR_UNSUPPORTED above), 1 <= G <= QL_MAX_GROUPS.
+ *   The result depends on nothing but index.
  */
 QL_API ql_status group_rows(const int32_t *index, int M, int G, int32_t *order, int32_t *offsets, void *workspace,
                             size_t ws_bytes, ql_stream_t stream);
@@ -374,7 +375,7 @@ QL_API size_t moe_route_workspace_bytes(int T, int E, int k);
  *   x      device bf16 bits [X][K], y device [Y][N] of y_dtype (round to nearest even of the fp32 sum).
  *   K % 4 == 0.  K % 64 == 0 runs on the tensor cores at every size; other K on the plain cores.
  *   The counts stay on the device: the host reads no offsets.  fp32 outputs are summed in pieces
- *   of 512 inputs whose sums are added in fp32 (the tensor cores' own running sum truncates).
+ *   of 512 inputs (K / 16 above K = 8192) whose sums are added in fp32 (the tensor cores' own running sum truncates).
  *   Alignment: codes, lut, x, y 16 bytes.
  */
 QL_API ql_status benq_grouped_linear(const uint8_t *codes, const uint16_t *lut, const ql_groups *groups,
@@ -409,14 +410,14 @@ QL_API ql_status moe_combine(const void *y, ql_out_dtype y_dtype, const int32_t 
  *   The projection (benq_linear, mdbf_linear, ...) has written y_s before; rows of no adapter keep
  *   it.  The inner sums are fp32 and enter the second product as a bf16 pair hi + lo (2^-17
  *   relative); an fp32 y takes one rounding of the sum, a bf16 y one rounding to nearest even.
- *   layers   host array of S entries (1 <= S <= 4) that read the same x.
+ *   layers   host array of S entries (1 <= S <= 4) that read the same x; no two with one y.
  *   x        device bf16 bits [T][K]; order device int32 [T], offsets device int32 [G + 1]: the plan
  *            of the rows' adapters (no row twice).
  *   scale    device fp32 [G] or NULL (all 1).
  *   r        the adapters' rank, 1 .. 256 (smaller ranks: zero rows of A).
  *   workspace  device, 256-byte aligned, at least lora_workspace_bytes(S, T, r) bytes; needs no clearing;
  *            not shared with a concurrent call.
- *   Alignment: A, B, x, y 16 bytes.  T >= 0, K >= 1 and N >= 1 of any size.
+ *   Alignment: A, B, x, y 16 bytes.  0 <= T <= QL_MAX_POSITIONS, K >= 1 and N >= 1 of any size.
  */
 typedef struct {
   const uint16_t *A;      /* bf16 [G][r][K] */

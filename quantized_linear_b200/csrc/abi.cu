@@ -396,6 +396,7 @@ static ql_status grouped(const char *who, const uint8_t *codes, const uint16_t *
   if (N <= 0 || K <= 0) return fail(QL_ERR_INVALID_ARG, "%s: N, K must be positive", who);
   if (K % 4) return fail(QL_ERR_INVALID_ARG, "%s: K = %d is not a multiple of 4", who, K);
   if ((int64_t)g->G * N >= ((int64_t)1 << 31)) return fail(QL_ERR_UNSUPPORTED, "%s: G * N must be below 2^31", who);
+  if (g->M > QL_MAX_POSITIONS) return fail(QL_ERR_UNSUPPORTED, "%s: M = %d is above %d", who, g->M, QL_MAX_POSITIONS);
   if (!dtype_ok(y_dtype)) return fail(QL_ERR_INVALID_ARG, "%s: bad output dtype", who);
   if (!codes || !lut || (pair && (!codes2 || !lut2)) || !g->offsets) return fail(QL_ERR_INVALID_ARG, "%s: null pointer", who);
   if (!aligned(g->offsets, 4) || !aligned(g->x_rows, 4) || !aligned(g->y_rows, 4))
@@ -455,7 +456,10 @@ ql_status lora_add(const lora_layer *layers, int S, const uint16_t *x, const int
     if (!L.A || !L.B || (T > 0 && !L.y)) return fail(QL_ERR_INVALID_ARG, "lora_add: null pointer in layer %d", i);
     if (!aligned(L.A, 16) || !aligned(L.B, 16) || !aligned(L.y, 16))
       return fail(QL_ERR_ALIGNMENT, "lora_add: A, B and y of layer %d must be 16-byte aligned", i);
+    for (int j = 0; j < i; ++j)
+      if (L.y && layers[j].y == L.y) return fail(QL_ERR_INVALID_ARG, "lora_add: layers %d and %d share one y", j, i);
   }
+  if (T > QL_MAX_POSITIONS) return fail(QL_ERR_UNSUPPORTED, "lora_add: T = %d is above %d", T, QL_MAX_POSITIONS);
   if (T == 0) return QL_OK;
   if (!x || !order || !offsets) return fail(QL_ERR_INVALID_ARG, "lora_add: null pointer");
   const ql_status st = check_workspace("lora_add", workspace, ws_bytes, ql::lora_workspace_size(S, T, r));

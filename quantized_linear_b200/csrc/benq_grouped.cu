@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(256)
   for (int64_t u = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; u < units;
        u += ((int64_t)gridDim.x * blockDim.x) >> 5) {
     const int g = (int)(u / N), n = (int)(u - (int64_t)g * N);
-    const int p0 = max(0, min(gr.M, gr.offsets[g])), p1 = max(0, min(gr.M, gr.offsets[g + 1]));
+    const int p0 = max(0, min(gr.M, __ldcg(gr.offsets + g))), p1 = max(0, min(gr.M, __ldcg(gr.offsets + g + 1)));
     for (int p = p0; p < p1; p += PB) {
       const uint16_t *xp[PB];
       int64_t yr[PB];
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256)
         xp[b] = nullptr;
         yr[b] = -1;
         if (p + b < p1) {
-          const int xi = gr.x_rows ? gr.x_rows[p + b] : p + b, yi = gr.y_rows ? gr.y_rows[p + b] : p + b;
+          const int xi = gr.x_rows ? __ldcg(gr.x_rows + p + b) : p + b, yi = gr.y_rows ? __ldcg(gr.y_rows + p + b) : p + b;
           if (xi >= 0 && xi / gr.x_div < gr.X && (unsigned)yi < (unsigned)gr.Y) {
             xp[b] = x + (int64_t)(gr.x_rows ? xi / gr.x_div : xi) * K;
             yr[b] = yi;
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256)
             const uint16_t w = t[(v >> (6 * e)) & 63];
 #pragma unroll
             for (int b = 0; b < PB; ++b)
-              if (xp[b]) acc[m][b] = qld::fma_bf16(w, xp[b][4 * q + e], acc[m][b]);
+              if (xp[b]) acc[m][b] = qld::fma_bf16(w, __ldcg(xp[b] + 4 * q + e), acc[m][b]);
           }
         }
       }

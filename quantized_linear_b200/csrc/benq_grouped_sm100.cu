@@ -279,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int g = g0 + lane;
       int n = 0;
       if (g < G) {
-        const int s0 = max(0, min(a.g.M, a.g.offsets[g])), s1 = max(0, min(a.g.M, a.g.offsets[g + 1]));
+        const int s0 = max(0, min(a.g.M, __ldcg(a.g.offsets + g))), s1 = max(0, min(a.g.M, __ldcg(a.g.offsets + g + 1)));
         n = s1 > s0 ? (s1 - s0 + a.nt_max - 1) / a.nt_max : 0;
       }
       int s = n;
@@ -298,7 +298,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   sm100::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_raw + OFF_MISC);
   const uint32_t a_col = tmem + 2 * a.slot;        // the stages of decoded W
-  const int nitems = cum[G] * a.ntl;
+  // (a plan whose groups overlap can have more tiles than any real one: the count stays within 31 bits)
+  const int nitems = (int)min((int64_t)cum[G] * a.ntl, (int64_t)1 << 30);
   auto tile_at = [&](int item) {
     Tile t;
     const int tt = item / a.ntl;
@@ -310,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     t.g = lo;
     const int s0 = max(0, min(a.g.M, __ldcg(a.g.offsets + lo))), s1 = max(0, min(a.g.M, __ldcg(a.g.offsets + lo + 1)));
-    const int nt = cum[lo + 1] - cum[lo], per = (s1 - s0 + nt - 1) / nt;   // a group's tiles are of equal length
+    const int nt = cum[lo + 1] - cum[lo], per = min(a.nt_max, (s1 - s0 + nt - 1) / nt);   // a group's tiles are of equal length
     t.p0 = s0 + (tt - cum[lo]) * per;
     t.p1 = min(s1, t.p0 + per);
     const int n = (per + 15) & ~15;
@@ -739,7 +740,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   }
 
-  if (!ok) atomicExch(&g_grouped_timeout, 1);
+  if (!ok) {
+    atomicExch(&g_grouped_timeout, 1);
+    settle();
+  }
   // neither CTA leaves while its peer may still arrive on its barriers or use its shared or tensor memory
   sm100::tc_fence_before();
   sm100::cluster_sync();

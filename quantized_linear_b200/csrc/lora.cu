@@ -49,7 +49,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int K) {
     uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0;
+      const uint32_t lo = k + 2 * i < K ? __ldcg(row + k + 2 * i) : 0, hi = k + 2 * i + 1 < K ? __ldcg(row + k + 2 * i + 1) : 0;
       v[i] = lo | (hi << 16);
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
@@ -268,7 +268,7 @@ __device__ __forceinline__ uint2 load4(const uint16_t *row, int k, int r, bool v
   return make_uint2(e0 | (e1 << 16), e2 | (e3 << 16));
 }
 
-// Tiles of 16 MTL positions; grid (runs of `rounds` feature rounds of all layers, tiles).  The y values of a strip are
+// Tiles of 16 MTL positions by runs of `rounds` feature rounds of a layer, tile after tile.  The y values of a strip are
 // requested before its products, so that the two overlap; B's rows come straight from memory, KC blocks of 16 ranks
 // at a time, the first of them before t is prepared.
 template <bool F32, int MTL>
@@ -279,12 +279,13 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
   extern __shared__ __align__(16) unsigned char esm[];   // t as bf16: [hi, lo][ET][rp], rows of rp * 2 bytes
   __shared__ int where[3], rows[ET];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int tile = blockIdx.x / L.chunk0[S], chunk = blockIdx.x - tile * L.chunk0[S];
   const int r16 = (r + 15) / 16, rp = r16 * 16 + 8;      // an odd number of 16-byte pieces: no bank conflicts
   qld::pdl_trigger();
   qld::pdl_wait();
   if (warp == 0) {
     int g, p0 = 0, p1 = 0;
-    find_tile(offsets, G, T, ET, blockIdx.y, g, p0, p1);
+    find_tile(offsets, G, T, ET, tile, g, p0, p1);
     if (lane == 0) where[0] = g, where[1] = p0, where[2] = p1;
     if (g >= 0) {
       for (int i = lane; i < ET; i += 32) {
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
   const int g = where[0], p0 = where[1], count = where[2] - p0;
   if (g < 0) return;
   int s = 0;
-  while (s + 1 < S && (int)blockIdx.x >= L.chunk0[s + 1]) ++s;
-  const int N = L.N[s], f0 = ((int)blockIdx.x - L.chunk0[s]) * rounds * EF;
+  while (s + 1 < S && chunk >= L.chunk0[s + 1]) ++s;
+  const int N = L.N[s], f0 = (chunk - L.chunk0[s]) * rounds * EF;
   const uint16_t *const B = L.B[s] + (int64_t)g * N * r;
   const int mt = MTL == 1 ? 1 : (count + 15) / 16;
   const bool vec = r % 4 == 0;                    // 8-byte aligned rows of B
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (n + i < N) y[i] += add[i];
+              if (n + i < N) y[i] = __ldcg(y + i) + add[i];
           }
         } else {
           uint16_t *y = static_cast<uint16_t *>(L.y[s]) + (size_t)row * N + n;
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (n + i < N) y[i] = qld::f32_to_bf16_rn(qld::bf16_to_f32(y[i]) + add[i]);
+              if (n + i < N) y[i] = qld::f32_to_bf16_rn(qld::bf16_to_f32(__ldcg(y + i)) + add[i]);
           }
         }
       }
@@ -487,7 +488,7 @@ ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, co
     auto kern = lora_expand_kernel<decltype(f32c)::value, decltype(mtl)::value>;
     const size_t smem = (size_t)2 * ET * ((r + 15) / 16 * 16 + 8) * 2;
     if (smem > 40 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
-    launch(kern, dim3(L.chunk0[S], tiles(ET)), WARPS * 32, smem, s, L, S, order, offsets, scale, G, T, r, shares, rounds,
+    launch(kern, dim3(L.chunk0[S] * tiles(ET)), WARPS * 32, smem, s, L, S, order, offsets, scale, G, T, r, shares, rounds,
            static_cast<const float *>(t));
     return true;
   };

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     sm100::tmem_alloc(tslot, 512);
     sm100::tmem_relinquish();
   }
+  __syncthreads();   // the next launch of this kernel may share the SM: this one's tensor memory comes first
   qld::pdl_trigger();
   qld::pdl_wait();
   if (warp == 0) {                                       // how many tiles there are
@@ -304,7 +305,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) sm100::mbar_arrive(d_free + 8 * d);
     }
   }
-  if (!ok) atomicExch(&g_lora_timeout, 1);
+  if (!ok) {
+    atomicExch(&g_lora_timeout, 1);
+    settle();
+  }
   sm100::tc_fence_before();
   __syncthreads();
   if (warp == WORK) {

@@ -190,7 +190,10 @@ __global__ void __launch_bounds__(THREADS + 32, 1)
       store8<OF32>(static_cast<char *>(out) + ((size_t)t * N + n) * OB, acc);
     }
   }
-  if (!ok) atomicExch(&g_combine_timeout, 1);
+  if (!ok) {
+    atomicExch(&g_combine_timeout, 1);
+    pairgemm::settle();
+  }
 }
 
 __device__ __forceinline__ float load1(const void *p, size_t i, bool f32) {

@@ -155,6 +155,7 @@ CASES = [
     ([1], 1, 4), ([1], 128, 64), ([0, 1, 0], 130, 64), ([3, 0, 5], 37, 100), ([2, 1], 64, 1000),
     ([1, 0, 8, 16, 17], 256, 128), ([33, 1, 0, 64], 200, 192), ([5] * 9, 129, 320), ([200, 3], 300, 256),
     ([193, 0, 385], 257, 576), ([1, 2], 1088, 5120), ([7, 1, 0, 20], 640, 1088), ([600], 96, 1024),
+    ([1, 3], 130, 17408), ([70], 40, 9216),
 ]
 
 
@@ -242,7 +243,8 @@ def test_bad_plans_stay_in_bounds(ql, K):
 
 # ------------------------------------------------------------------------------------------- combine
 
-@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (1, 8, 5120), (3, 2, 7), (65, 8, 1088), (300, 5, 513), (17, 32, 64)])
+@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (1, 8, 5120), (3, 2, 7), (65, 8, 1088), (300, 5, 513), (17, 32, 64),
+                                   (900, 3, 4104), (400, 20, 2056), (40, 9, 16)])   # many rounds of the ring, groups of rows
 @pytest.mark.parametrize("ydt", DTYPES)
 @pytest.mark.parametrize("odt", DTYPES)
 def test_moe_combine(ql, T, k, N, ydt, odt):

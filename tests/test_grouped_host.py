@@ -74,6 +74,7 @@ def test_grouped_refusals(ql, gated):
     assert call(_groups(ql), y=A + 4) == ql.QL_ERR_ALIGNMENT
     assert call(_groups(ql, x_rows=A + 2)) == ql.QL_ERR_ALIGNMENT
     assert call(_groups(ql, G=1024), N=1 << 22) == ql.QL_ERR_UNSUPPORTED
+    assert call(_groups(ql, M=(1 << 24) + 1)) == ql.QL_ERR_UNSUPPORTED
     assert call(_groups(ql, M=0), x=None, y=None) == ql.QL_OK    # no positions: nothing to do
 
 
@@ -111,6 +112,9 @@ def test_lora_refusals(ql):
     assert call() == ql.QL_ERR_INVALID_ARG
     arr[0] = ql.LoraLayerC(A, A, A, 8)
     assert call(T=0, x=None, order=None, offsets=None) == ql.QL_OK
+    assert call(T=(1 << 24) + 1, nbytes=1 << 40) == ql.QL_ERR_UNSUPPORTED
+    # two layers that would add to one y at the same time
+    assert call(S=2, nbytes=1 << 20) == ql.QL_ERR_INVALID_ARG and b"share one y" in ql.lib().ql_last_error()
 
 
 def test_binding_refuses_wrong_tensors(ql):

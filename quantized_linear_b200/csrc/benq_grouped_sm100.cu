@@ -74,9 +74,9 @@ constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
 constexpr int OFF_C = OFF_X + X_RING;
 constexpr int STG_BYTES = 1024;                // per epilogue warp: 16 positions x 32 features of bf16
 constexpr int OFF_STG = OFF_C + SC * C_BYTES;
-constexpr int OFF_ROW = OFF_STG + 4 * STG_BYTES;      // per x warp: the gathered rows of its part, int [XLIST]
+constexpr int OFF_ROW = OFF_STG + 8 * STG_BYTES;      // per x warp: the gathered rows of its part, int [XLIST]
 constexpr int XLIST = (NT / 2 / 4 + XPARTS - 1) / XPARTS * 4;   // rows of a part, at most
-constexpr int OFF_YROW = OFF_ROW + 2 * XPARTS * XLIST * 4;        // per epilogue warp: the output rows of a slot, int [NT / 2]
+constexpr int OFF_YROW = OFF_ROW + 2 * XPARTS * XLIST * 4;        // per quarter of tensor memory: the output rows of a slot, int [NT / 2]
 constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * (NT / 2) * 4;
 static_assert(OFF_GRP + (QL_MAX_GROUPS + 1) * 4 <= FRONT, "front");
 static_assert(D_MAX + 64 * 4 <= 512, "tensor memory: four stages of decoded W beside the accumulators");
@@ -248,6 +248,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int nkb = a.K / 64, nst = (nkb + 1) / 2;   // K blocks, steps
   const uint32_t xblk = a.xr * 128;                // bytes of a 64-column block of an x stage
+  const bool gathered = a.g.x_rows != nullptr;
+  const int sets = gathered ? 1 : 2;               // warps 24-27 gather x rows, or are a second set of epilogue warps
   bool ok = true;
   // a wait of a whole warp: no lane goes on alone when one gave up
   auto warp_wait = [&](uint32_t b, uint32_t parity, unsigned nap) {
@@ -271,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       sm100::mbar_init(bar.tbl_full + 8 * s, 1);
       sm100::mbar_init(bar.tbl_empty + 8 * s, NDW);
       sm100::mbar_init(bar.acc_full + 8 * s, 1);
-      sm100::mbar_init(bar.acc_empty + 8 * s, 2 * 4);
+      sm100::mbar_init(bar.acc_empty + 8 * s, 2 * 4 * sets);
     }
     sts32(tmem_slot + 4, 0);
     sm100::fence_barrier_init();
@@ -333,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     return t;
   };
 
-  if (warp == 0 || warp == 3 || warp >= 8 + NDW) {
+  if (warp == 0 || warp == 3 || (warp >= 8 + NDW && gathered)) {
     // ------------------------------------------------------------ x producer
     const uint32_t lead_full = sm100::mapa_shared(bar.full_x, 0);
     int st = 0;
@@ -384,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (i0 + i < g1) sm100::tma_gather4_pair(dst + (i0 + i) * 512, &map_x, kx, y[i], full);
             }
           } else {                               // rows past the tile are other rows, whose columns are not stored
-            for (int j = part; j < t.halves * boxes; j += XPARTS) {
+            for (int j = 0; j < t.halves * boxes; ++j) {
               const int h = j >= boxes;
               sm100::tma_load_2d_pair(dst + j * X_BOX * 128, &map_x, kx,
                                       t.p0 + h * t.nh + (int)rank * nr + (j - (h ? boxes : 0)) * X_BOX, full);
@@ -553,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         while (ok && q < 4) store(b);
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 8 && warp < 8 + NDW) {
     // ------------------------------------------------------------ decoders
     // Warpgroup wg takes every fourth step, both of its K blocks.  A row's codes are a stream of 16-byte chunks, eight to
     // a line (stage), six to a step: four steps are three lines, so that within a tile a warpgroup always finds its
@@ -627,9 +629,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(bar.tbl_empty + 8 * (tl & 1));
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;                    // this warp's lanes of tensor memory
+    // Warps 4-7, and 24-27 where x needs no gathering: then the sets take turns at chunks of 16 positions.  (4096 tokens
+    // through 64 experts of K 1088: the MMAs wait for a tile's epilogue a third of the time with one set.)
+    const int q = warp & 3, c0 = warp >= 8 ? 16 : 0, cstep = 16 * sets;   // this warp's lanes of tensor memory, its chunks
     const uint32_t lead_empty = sm100::mapa_shared(bar.acc_empty, 0);
     Slots sl;
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
@@ -644,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // the output rows of the slot's positions, -1 for none: read while the products run
       const uint32_t ylist = sbase + OFF_YROW + q * (NT / 2) * 4;
       __syncwarp();
-      for (int i = lane; i < t.nh; i += 32) {
+      for (int i = c0 + (lane >> 4) * cstep + (lane & 15); i < t.nh; i += 2 * cstep) {
         const int p = pbase + i;
         int yr = -1;
         if (p < t.p1) {
@@ -667,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // their way through this warp's own kilobyte of shared memory, leave as 16-byte stores.  One store and a
         // half per 8 columns instead of 8 shuffles and 8 two-byte stores: those queue behind the decoders' lookups.
         constexpr int FW = GATED ? 16 : 32;    // features of this warp
-        const uint32_t stg = sbase + OFF_STG + (warp - 4) * STG_BYTES;
+        const uint32_t stg = sbase + OFF_STG + (q + (c0 ? 4 : 0)) * STG_BYTES;
         // matrices of 8 features x 8 positions, thread i giving row i % 8 (a position) of matrix i / 8.  The 16-byte
         // pieces of a position are permuted so that 8 positions share no bank.
         constexpr int PP = FW / 8, NP = 32 / PP;   // 16-byte pieces per position, positions per round
@@ -677,9 +681,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int mpos = GATED ? (lane & 7) + ((lane >> 4) << 3) : lane & 7, mf = GATED ? (lane >> 3) & 1 : lane >> 3;
         const int nb = (t.wt * 2 + (int)rank) * (GATED ? RW / 2 : RW) + FW * q;   // this warp's first feature
         uint32_t lo[8], hi[8];                 // lanes 0-15 and 16-31 of this warp's quarter
-        sm100::tmem_ld_16x256b_x2(acc, lo);
-        sm100::tmem_ld_16x256b_x2(acc + (16u << 16), hi);
-        for (int c = 0; c < t.nh; c += 16) {
+        if (c0 < t.nh) {
+          sm100::tmem_ld_16x256b_x2(acc + c0, lo);
+          sm100::tmem_ld_16x256b_x2(acc + c0 + (16u << 16), hi);
+        }
+        for (int c = c0; c < t.nh; c += cstep) {
           sm100::tmem_wait_ld();
           if constexpr (GATED) {               // lo is g and hi is u of the same features and positions
 #pragma unroll
@@ -691,9 +697,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             w[GATED ? i : (i >> 1) * 4 + (i & 1)] = pack2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]), OUT_BF16);
             if constexpr (!GATED) w[(i >> 1) * 4 + 2 + (i & 1)] = pack2(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]), OUT_BF16);
           }
-          if (c + 16 < t.nh) {
-            sm100::tmem_ld_16x256b_x2(acc + c + 16, lo);
-            sm100::tmem_ld_16x256b_x2(acc + c + 16 + (16u << 16), hi);
+          if (c + cstep < t.nh) {
+            sm100::tmem_ld_16x256b_x2(acc + c + cstep, lo);
+            sm100::tmem_ld_16x256b_x2(acc + c + cstep + (16u << 16), hi);
           }
           __syncwarp();                        // the last chunk has been read out of the staging
 #pragma unroll
@@ -712,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
       } else {
-      for (int c = 0; c < t.nh; c += 16) {
+      for (int c = c0; c < t.nh; c += cstep) {
         uint32_t v[16];
         sm100::tmem_ld_32x32b_x16(acc + c, v);
         sm100::tmem_wait_ld();

@@ -70,15 +70,16 @@ constexpr int FRONT = 8192 - 1024;
 constexpr int NBAR = 2 * SX_MAX + 2 * SA_MAX + 2 * SC + 8;
 constexpr int OFF_MISC = NBAR * 8;             // tensor-memory address, abort flag
 constexpr int OFF_GRP = OFF_MISC + 16;         // token tiles before each group, int [G + 1]
+constexpr int OFF_Y1 = (OFF_GRP + (QL_MAX_GROUPS + 1) * 4 + 15) / 16 * 16;   // the second half's output rows (see OFF_YROW)
 constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
 constexpr int OFF_C = OFF_X + X_RING;
 constexpr int STG_BYTES = 1024;                // per epilogue warp: 16 positions x 32 features of bf16
 constexpr int OFF_STG = OFF_C + SC * C_BYTES;
 constexpr int OFF_ROW = OFF_STG + 8 * STG_BYTES;      // per x warp: the gathered rows of its part, int [XLIST]
 constexpr int XLIST = (NT / 2 / 4 + XPARTS - 1) / XPARTS * 4;   // rows of a part, at most
-constexpr int OFF_YROW = OFF_ROW + 2 * XPARTS * XLIST * 4;        // per quarter of tensor memory: the output rows of a slot, int [NT / 2]
+constexpr int OFF_YROW = OFF_ROW + 2 * XPARTS * XLIST * 4;        // per quarter of tensor memory: the output rows of a tile's first half, int [NT / 2]
 constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * (NT / 2) * 4;
-static_assert(OFF_GRP + (QL_MAX_GROUPS + 1) * 4 <= FRONT, "front");
+static_assert(OFF_Y1 + 4 * (NT / 2) * 4 <= FRONT, "front");
 static_assert(D_MAX + 64 * 4 <= 512, "tensor memory: four stages of decoded W beside the accumulators");
 static_assert(OFF_X % 1024 == 0 && OFF_C % 128 == 0 && C_BYTES % 1024 == 0 && OFF_C % 1024 == 0 && OFF_STG % 128 == 0, "alignment");
 static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -643,22 +644,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       sl.done(first_slot, slots);
       const int n = GATED ? (t.wt * 2 + (int)rank) * (RW / 2) + 16 * q + (lane & 15)
                           : (t.wt * 2 + (int)rank) * RW + 32 * q + lane;
-      for (int h = 0; h < t.halves && ok; ++h) {
-      const int es = first_slot + h, pbase = t.p0 + h * t.nh;
-      // the output rows of the slot's positions, -1 for none: read while the products run
-      const uint32_t ylist = sbase + OFF_YROW + q * (NT / 2) * 4;
+      // the output rows of the tile's positions, -1 for none: read while the products run
+      const uint32_t ylist0 = sbase + OFF_YROW + q * (NT / 2) * 4, ylist1 = raw + OFF_Y1 + q * (NT / 2) * 4;
       __syncwarp();
-      for (int i = c0 + (lane >> 4) * cstep + (lane & 15); i < t.nh; i += 2 * cstep) {
-        const int p = pbase + i;
-        int yr = -1;
-        if (p < t.p1) {
-          const int xi = a.g.x_rows ? __ldcg(a.g.x_rows + p) : p;
-          yr = a.g.y_rows ? __ldcg(a.g.y_rows + p) : p;
-          if ((unsigned)yr >= (unsigned)a.g.Y || xi < 0 || (a.g.x_rows ? xi / a.g.x_div : xi) >= a.g.X) yr = -1;
+      for (int h = 0; h < t.halves; ++h)
+        for (int i = c0 + (lane >> 4) * cstep + (lane & 15); i < t.nh; i += 2 * cstep) {
+          const int p = t.p0 + h * t.nh + i;
+          int yr = -1;
+          if (p < t.p1) {
+            const int xi = a.g.x_rows ? __ldcg(a.g.x_rows + p) : p;
+            yr = a.g.y_rows ? __ldcg(a.g.y_rows + p) : p;
+            if ((unsigned)yr >= (unsigned)a.g.Y || xi < 0 || (a.g.x_rows ? xi / a.g.x_div : xi) >= a.g.X) yr = -1;
+          }
+          sts32((h ? ylist1 : ylist0) + 4 * i, (uint32_t)yr);
         }
-        sts32(ylist + 4 * i, (uint32_t)yr);
-      }
       __syncwarp();
+      for (int h = 0; h < t.halves && ok; ++h) {
+      const int es = first_slot + h;
+      const uint32_t ylist = h ? ylist1 : ylist0;
       if (!warp_wait(bar.acc_full + 8 * es, (es ? used1 : used0) & 1, LONG_NAP) ||
           (runs && !warp_wait(bar.acc_full + 8, used1 & 1, LONG_NAP))) {
         ok = false;

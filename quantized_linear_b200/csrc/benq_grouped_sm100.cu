@@ -49,16 +49,16 @@ using namespace pairgemm;
 
 constexpr int RW = 128;                        // rows of W per CTA and tile
 constexpr int NT = 256;                        // positions per tile at most (two MMAs of half as many, N)
-constexpr int SA_MAX = 6, SC = 3;              // stages: decoded W (steps, as many as tensor memory has room for, at
-                                               // least one per decoder warpgroup), codes
-constexpr int X_RING = 96 * 1024;              // x stages of one step each: two 64-column blocks of half a tile's rows
-constexpr int SX_MAX = 8;
+constexpr int SA_MAX = 6;                      // stages of decoded W (steps): as many as tensor memory has room for, at
+                                               // least one per decoder warpgroup
+constexpr int XC_RING = 144 * 1024;            // x stages of one step each (two 64-column blocks of half a tile's rows),
+constexpr int SX_MAX = 6, SC_MIN = 3, SC_MAX = 6;   // and then code stages
 constexpr int X_BOX = 32;                      // rows per copy when rows are not gathered
 constexpr int C_LINE = 128;                    // code bytes per row and stage: 128-byte rows in the 128-byte swizzle.  (Unswizzled
 constexpr int C_BYTES = RW * C_LINE;           // 144-byte rows, three K blocks, took the TMA unit 21 clocks each.)  16 KB
 constexpr int TBL_BYTES = 4 * 8192;            // lane-private tables: 4 warps of rows x [64][32] words, two buffers
 constexpr int NDW = 16;                        // decoder warps: four warpgroups, two per step in turn
-constexpr int XPARTS = 3;                      // warps that copy a K block's x rows
+constexpr int XPARTS = 3;                      // pairs of warps that gather x rows, a step each in turn
 constexpr int THREADS = (8 + NDW + 2 * (XPARTS - 1)) * 32;
 constexpr int D_MAX = 256;                     // tensor memory columns: at most these are accumulators, then steps of 2 x 32
 constexpr int MAX_SEG = D_MAX / 16;            // runs of K blocks with an accumulator each (fp32 outputs)
@@ -67,22 +67,21 @@ constexpr int SEG_STEPS = 4;                   // 512 inputs
 // the address).  The front's size puts them there when dynamic shared memory starts at 1 KB, as it does after the
 // kilobyte that the system keeps; the kernel checks it.
 constexpr int FRONT = 8192 - 1024;
-constexpr int NBAR = 2 * SX_MAX + 2 * SA_MAX + 2 * SC + 8;
+constexpr int NBAR = 2 * SX_MAX + 2 * SA_MAX + 2 * SC_MAX + 8;
 constexpr int OFF_MISC = NBAR * 8;             // tensor-memory address, abort flag
 constexpr int OFF_GRP = OFF_MISC + 16;         // token tiles before each group, int [G + 1]
 constexpr int OFF_Y1 = (OFF_GRP + (QL_MAX_GROUPS + 1) * 4 + 15) / 16 * 16;   // the second half's output rows (see OFF_YROW)
 constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
-constexpr int OFF_C = OFF_X + X_RING;
 constexpr int STG_BYTES = 1024;                // per epilogue warp: 16 positions x 32 features of bf16
-constexpr int OFF_STG = OFF_C + SC * C_BYTES;
-constexpr int OFF_ROW = OFF_STG + 8 * STG_BYTES;      // per x warp: the gathered rows of its part, int [XLIST]
-constexpr int XLIST = (NT / 2 / 4 + XPARTS - 1) / XPARTS * 4;   // rows of a part, at most
-constexpr int OFF_YROW = OFF_ROW + 2 * XPARTS * XLIST * 4;        // per quarter of tensor memory: the output rows of a tile's first half, int [NT / 2]
+constexpr int OFF_STG = OFF_X + XC_RING;
+constexpr int OFF_ROW = OFF_STG + 4 * STG_BYTES;      // in place of the second set's staging: per x warp, the rows that it
+                                                      // gathers, int [NT / 2]
+constexpr int OFF_YROW = OFF_STG + 8 * STG_BYTES;     // per quarter of tensor memory: the output rows of a tile's first half, int [NT / 2]
 constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * (NT / 2) * 4;
 static_assert(OFF_Y1 + 4 * (NT / 2) * 4 <= FRONT, "front");
 static_assert(D_MAX + 64 * 4 <= 512, "tensor memory: four stages of decoded W beside the accumulators");
-static_assert(OFF_X % 1024 == 0 && OFF_C % 128 == 0 && C_BYTES % 1024 == 0 && OFF_C % 1024 == 0 && OFF_STG % 128 == 0, "alignment");
-static_assert(SMEM_BYTES <= 232448, "shared memory");
+static_assert(OFF_X % 1024 == 0 && C_BYTES % 1024 == 0 && OFF_STG % 128 == 0, "alignment");
+static_assert(2 * XPARTS * (NT / 2) * 4 <= 4 * STG_BYTES && SMEM_BYTES <= 232448, "shared memory");
 constexpr uint16_t PAIR = 0x3;
 constexpr unsigned NAP = 32, LONG_NAP = 128;   // ns between tries of warps that run ahead, and of the epilogue
 
@@ -94,7 +93,7 @@ struct Bars {
   uint32_t full_x, empty_x, ready_a, empty_a, full_c, empty_c, tbl_full, tbl_empty, acc_full, acc_empty;
   __device__ Bars(uint32_t b)
       : full_x(b), empty_x(full_x + 8 * SX_MAX), ready_a(empty_x + 8 * SX_MAX), empty_a(ready_a + 8 * SA_MAX),
-        full_c(empty_a + 8 * SA_MAX), empty_c(full_c + 8 * SC), tbl_full(empty_c + 8 * SC), tbl_empty(tbl_full + 8 * 2),
+        full_c(empty_a + 8 * SA_MAX), empty_c(full_c + 8 * SC_MAX), tbl_full(empty_c + 8 * SC_MAX), tbl_empty(tbl_full + 8 * 2),
         acc_full(tbl_empty + 8 * 2), acc_empty(acc_full + 8 * 2) {}
 };
 
@@ -103,7 +102,7 @@ struct Args {
   ql_groups g;
   void *y;
   int ydt, N, K, ntl, nt_max;   // tiles of W rows per group, positions per tile at most
-  int xr, xst;                       // rows per 64-column block of an x stage, x stages
+  int xr, xst, sc;                   // rows per 64-column block of an x stage, x stages, code stages
   int slot, sa;                      // columns of each of the two accumulator slots, stages of decoded W behind them
   int vec;                           // bf16 rows of whole 16-byte pieces
   int seg, nseg;                     // steps per run of its own accumulator, runs
@@ -205,6 +204,17 @@ __device__ __forceinline__ bool try_wait8(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether a barrier's phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The bounded wait of this kernel (as pairgemm::Waiter): gives up when the budget runs out or the pair's abort flag is
 // set, and then sets it in both CTAs.  nap: nanoseconds between rounds of tries, for warps that run ahead of the others.
 struct Wait {
@@ -249,6 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int nkb = a.K / 64, nst = (nkb + 1) / 2;   // K blocks, steps
   const uint32_t xblk = a.xr * 128;                // bytes of a 64-column block of an x stage
+  const uint32_t cring = sbase + OFF_X + 2 * a.xst * xblk;   // the code stages
   const bool gathered = a.g.x_rows != nullptr;
   const int sets = gathered ? 1 : 2;               // warps 24-27 gather x rows, or are a second set of epilogue warps
   bool ok = true;
@@ -266,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       sm100::mbar_init(bar.ready_a + 8 * s, 2 * 4);     // a decoder warpgroup of each CTA
       sm100::mbar_init(bar.empty_a + 8 * s, 1);
     }
-    for (int s = 0; s < SC; ++s) {
+    for (int s = 0; s < SC_MAX; ++s) {
       sm100::mbar_init(bar.full_c + 8 * s, 1);
       sm100::mbar_init(bar.empty_c + 8 * s, 2 * 4);     // two steps' warps
     }
@@ -340,61 +351,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ x producer
     const uint32_t lead_full = sm100::mapa_shared(bar.full_x, 0);
     int st = 0;
-    // of each step, half of the x warps copy the first K block and half the second, each a part of its rows
-    const int xi = warp == 0 ? 0 : warp == 3 ? 1 : warp - (8 + NDW) + 2, b = xi & 1, part = xi >> 1;
+    // Of each step one x warp copies the first K block and one the second.  Pairs of gathering warps take turns: a warp
+    // needs 1100 clocks for a step however few its rows, most of them behind the decoders' lookups.  (As with decoded W, a
+    // phase's parity tells enough as long as there are no fewer stages than turns.)
+    const int xi = warp == 0 ? 0 : warp == 3 ? 1 : warp - (8 + NDW) + 2, b = xi & 1, parts = gathered ? XPARTS : 1;
+    int turn = xi >> 1;                        // steps until this warp's next
     uint32_t ph = 1;                           // a fresh barrier passes a wait for the phase before its first
     for (int wi = pair; wi < nitems && ok; wi += npairs) {
       const Tile t = tile_at(wi);
       const int nr = t.nh / 2;                 // rows of this CTA per half
       const int boxes = (nr + X_BOX - 1) / X_BOX;
-      const int rows = a.g.x_rows ? nr : boxes * X_BOX;   // rows copied per half
-      // gathered rows, both halves' one after the other, in groups of four, of which this warp has g0 .. g1 - 1: a place
-      // past the tile or a row out of range reads row 0, whose column is not stored
-      const uint32_t list = sbase + OFF_ROW + xi * XLIST * 4;
-      const int groups = t.halves * nr / 4, g0 = groups * part / XPARTS, g1 = groups * (part + 1) / XPARTS;
-      if (a.g.x_rows) {
+      const int rows = gathered ? nr : boxes * X_BOX;   // rows copied per half
+      // gathered rows, both halves' one after the other, in groups of four: a place past the tile or a row out of range
+      // reads row 0, whose column is not stored
+      const uint32_t list = sbase + OFF_ROW + xi * (NT / 2) * 4;
+      const int groups = t.halves * nr / 4;
+      if (gathered) {
         __syncwarp();
-        for (int i = 4 * g0 + lane; i < 4 * g1; i += 32) {
+        for (int i = lane; i < 4 * groups; i += 32) {
           const int h = i >= nr, p = t.p0 + h * t.nh + (int)rank * nr + i - (h ? nr : 0);
           int x = 0;
           if (p < t.p1) x = __ldcg(a.g.x_rows + p) / a.g.x_div;
-          sts32(list + 4 * (i - 4 * g0), (unsigned)x < (unsigned)a.g.X ? x : 0);
+          sts32(list + 4 * i, (unsigned)x < (unsigned)a.g.X ? x : 0);
         }
         __syncwarp();
       }
       for (int sp = 0; sp < nst; ++sp) {
         const int blocks = min(2, nkb - 2 * sp), kx = (2 * sp + b) * 64;
-        if (!warp_wait(bar.empty_x + 8 * st, ph, NAP)) { ok = false; break; }
-        if (b < blocks && sm100::elect_one()) {
-          const uint32_t dst = sbase + OFF_X + (2 * st + b) * xblk, full = lead_full + 8 * st;
-          if (lead && xi == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
-          if (a.g.x_rows) {
-            // the next four lists are loaded while four copies are issued (50 clocks each)
-            uint32_t r[4][4];
-            auto load = [&](int i0) {
+        if (turn-- == 0) {
+          turn = parts - 1;
+          if (!warp_wait(bar.empty_x + 8 * st, ph, NAP)) { ok = false; break; }
+          if (b < blocks && sm100::elect_one()) {
+            const uint32_t dst = sbase + OFF_X + (2 * st + b) * xblk, full = lead_full + 8 * st;
+            if (lead && b == 0) sm100::mbar_arrive_expect_tx(bar.full_x + 8 * st, 2 * t.halves * blocks * rows * 128);
+            if (gathered) {
+              // the next four lists are loaded while four copies are issued (50 clocks each)
+              uint32_t r[4][4];
+              auto load = [&](int i0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i0 + i < g1) lds128(list + 16 * (i0 + i - g0), r[i][0], r[i][1], r[i][2], r[i][3]);
-            };
-            load(g0);
-            for (int i0 = g0; i0 < g1; i0 += 4) {
-              int4 y[4];
+                for (int i = 0; i < 4; ++i)
+                  if (i0 + i < groups) lds128(list + 16 * (i0 + i), r[i][0], r[i][1], r[i][2], r[i][3]);
+              };
+              load(0);
+              for (int i0 = 0; i0 < groups; i0 += 4) {
+                int4 y[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) y[i] = make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]);
-              load(i0 + 4);
+                for (int i = 0; i < 4; ++i) y[i] = make_int4((int)r[i][0], (int)r[i][1], (int)r[i][2], (int)r[i][3]);
+                load(i0 + 4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i0 + i < g1) sm100::tma_gather4_pair(dst + (i0 + i) * 512, &map_x, kx, y[i], full);
-            }
-          } else {                               // rows past the tile are other rows, whose columns are not stored
-            for (int j = 0; j < t.halves * boxes; ++j) {
-              const int h = j >= boxes;
-              sm100::tma_load_2d_pair(dst + j * X_BOX * 128, &map_x, kx,
-                                      t.p0 + h * t.nh + (int)rank * nr + (j - (h ? boxes : 0)) * X_BOX, full);
+                for (int i = 0; i < 4; ++i)
+                  if (i0 + i < groups) sm100::tma_gather4_pair(dst + (i0 + i) * 512, &map_x, kx, y[i], full);
+              }
+            } else {                             // rows past the tile are other rows, whose columns are not stored
+              for (int j = 0; j < t.halves * boxes; ++j) {
+                const int h = j >= boxes;
+                sm100::tma_load_2d_pair(dst + j * X_BOX * 128, &map_x, kx,
+                                        t.p0 + h * t.nh + (int)rank * nr + (j - (h ? boxes : 0)) * X_BOX, full);
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
         if (++st == a.xst) {
           st = 0;
           ph ^= 1;
@@ -402,10 +419,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lead) {
-      // ---------------------------------------------------------- MMA issuer (even CTA)
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    // One lane does it all.  A look at a barrier takes 180 clocks behind the decoders' lookups even when its phase has
+    // long completed, so the next step's two are looked at before this step's MMAs are issued.
+    if (lead && sm100::elect_one()) {
       int sx = 0, sa = 0;
       uint32_t phx = 0, pha = 0;
+      bool seen = false;                       // the coming step's x and W are there
       Slots sl;
       const uint64_t xdesc = sm100::sw128_kmajor_desc(sbase + OFF_X);   // + address / 16 (below 2^14: no carry)
       for (int wi = pair; wi < nitems && ok; wi += npairs) {
@@ -413,24 +433,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int slots = a.nseg > 1 ? 2 : t.halves, first_slot = sl.take(slots);
         // a tile of two slots waits for the second one when its first step has multiplied into the first
         const bool wait1 = first_slot + slots == 2 && sl.used1 > 0, late1 = t.halves == 2;
-        if ((first_slot == 0 && sl.used0 > 0 && !warp_wait(bar.acc_empty, (sl.used0 - 1) & 1, 0)) ||
-            (wait1 && !late1 && !warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, 0))) {
+        if ((first_slot == 0 && sl.used0 > 0 && !wt(bar.acc_empty, (sl.used0 - 1) & 1, 0)) ||
+            (wait1 && !late1 && !wt(bar.acc_empty + 8, (sl.used1 - 1) & 1, 0))) {
           ok = false;
           break;
         }
-        sm100::tc_fence_after();
         const uint32_t idesc = sm100::idesc_bf16_f32(256, t.nh);
         // the second half's x rows follow the first's (whole copies when they are not gathered)
-        const uint32_t half = (a.g.x_rows ? t.nh / 2 : (t.nh / 2 + X_BOX - 1) / X_BOX * X_BOX) * 128 >> 4;
+        const uint32_t half = (gathered ? t.nh / 2 : (t.nh / 2 + X_BOX - 1) / X_BOX * X_BOX) * 128 >> 4;
         uint32_t d0 = tmem + first_slot * a.slot;
         int left = a.seg;                      // steps left in this run
         uint32_t add = 0;                      // 0 for the first MMA of a run, which overwrites
         for (int sp = 0; sp < nst; ++sp) {
-          if (!warp_wait(bar.full_x + 8 * sx, phx, 0) || !warp_wait(bar.ready_a + 8 * sa, pha, 0)) { ok = false; break; }
+          if (!seen && !(wt(bar.full_x + 8 * sx, phx, 0) && wt(bar.ready_a + 8 * sa, pha, 0))) { ok = false; break; }
           sm100::tc_fence_after();
           const int blocks = min(2, nkb - 2 * sp);
-          const uint32_t at0 = a_col + sa * 64;
+          const uint32_t at0 = a_col + sa * 64, ex = bar.empty_x + 8 * sx, ea = bar.empty_a + 8 * sa;
           const uint64_t bd0 = xdesc + (sx * 2 * xblk >> 4);
+          if (++sx == a.xst) {
+            sx = 0;
+            phx ^= 1;
+          }
+          if (++sa == a.sa) {
+            sa = 0;
+            pha ^= 1;
+          }
+          const bool seen_x = mbar_test(bar.full_x + 8 * sx, phx), seen_a = mbar_test(bar.ready_a + 8 * sa, pha);
           auto mmas = [&](uint32_t d, uint64_t bd) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -440,45 +468,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 sm100::mma_f16kind_pair_ts(d, at0 + b * 32 + kk * 8, bd + (b * xblk >> 4) + 2 * kk, idesc, add | kk | b);
             }
           };
-          if (sm100::elect_one()) mmas(d0, bd0);
-          __syncwarp();
+          mmas(d0, bd0);
           if (t.halves == 2) {
             if (sp == 0 && wait1) {
-              if (!warp_wait(bar.acc_empty + 8, (sl.used1 - 1) & 1, 0)) { ok = false; break; }
+              if (!wt(bar.acc_empty + 8, (sl.used1 - 1) & 1, 0)) { ok = false; break; }
               sm100::tc_fence_after();
             }
-            if (sm100::elect_one()) mmas(d0 + a.slot, bd0 + half);
-            __syncwarp();
+            mmas(d0 + a.slot, bd0 + half);
           }
-          if (sm100::elect_one()) {
-            sm100::mma_commit_pair(bar.empty_x + 8 * sx, PAIR);
-            sm100::mma_commit_pair(bar.empty_a + 8 * sa, PAIR);
-          }
-          __syncwarp();
+          sm100::mma_commit_pair(ex, PAIR);
+          sm100::mma_commit_pair(ea, PAIR);
           add = 1;
           if (--left == 0) {                   // the next run has an accumulator of its own
             left = a.seg;
             add = 0;
             d0 += t.nh;
           }
-          if (++sx == a.xst) {
-            sx = 0;
-            phx ^= 1;
-          }
-          if (++sa == a.sa) {
-            sa = 0;
-            pha ^= 1;
-          }
+          seen = seen_x && seen_a;
         }
         if (!ok) break;
-        if (sm100::elect_one()) {
-          if (first_slot == 0) sm100::mma_commit_pair(bar.acc_full, PAIR);
-          if (first_slot + slots == 2) sm100::mma_commit_pair(bar.acc_full + 8, PAIR);
-        }
-        __syncwarp();
+        if (first_slot == 0) sm100::mma_commit_pair(bar.acc_full, PAIR);
+        if (first_slot + slots == 2) sm100::mma_commit_pair(bar.acc_full + 8, PAIR);
         sl.done(first_slot, slots);
       }
     }
+    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------ codes, and the next tile's tables
     constexpr int per = GATED ? RW / 2 : RW;
@@ -532,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!warp_wait(bar.empty_c + 8 * sc, phc, NAP)) { ok = false; break; }
         if (sm100::elect_one()) {
           if (n0 < a.N) {
-            const uint32_t dst = sbase + OFF_C + sc * C_BYTES;
+            const uint32_t dst = cring + sc * C_BYTES;
             sm100::mbar_arrive_expect_tx(bar.full_c + 8 * sc, C_BYTES);
             sm100::tma_load_2d(dst, &map_c, ln * C_LINE, row0, bar.full_c + 8 * sc);
             if (GATED) sm100::tma_load_2d(dst + C_BYTES / 2, &map_c2, ln * C_LINE, row0, bar.full_c + 8 * sc);
@@ -541,12 +555,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         }
         __syncwarp();
-        if (++sc == SC) {
+        if (++sc == a.sc) {
           sc = 0;
           phc ^= 1;
         }
-        // Past SC stages the decoders are on this tile, so the buffer of the one before is free.
-        if (q < 4 && ln >= SC) {
+        // Past a.sc stages the decoders are on this tile, so the buffer of the one before is free.
+        if (q < 4 && ln >= a.sc) {
           if (q == 0 && tl >= 1 && !warp_wait(bar.tbl_empty + 8 * b, ((tl - 1) >> 1) & 1, NAP)) { ok = false; break; }
           store(b);
         }
@@ -560,11 +574,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ decoders
     // Warpgroup wg takes every fourth step, both of its K blocks.  A row's codes are a stream of 16-byte chunks, eight to
     // a line (stage), six to a step: four steps are three lines, so that within a tile a warpgroup always finds its
-    // chunks in the same places of the same stages, a phase further each time.
+    // chunks in the same places of a line, three lines further each time.
     const int q = warp & 3, wg = (warp >> 2) - 2;
     // the row of the staged codes that this lane decodes
     const int row = GATED ? (lane < 16 ? 0 : RW / 2) + 16 * q + (lane & 15) : 32 * q + lane;
-    const uint32_t crow = sbase + OFF_C + row * C_LINE;
+    const uint32_t crow = cring + row * C_LINE;
     const uint32_t ready = sm100::mapa_shared(bar.ready_a, 0);
     const uint32_t to = a_col + ((uint32_t)(32 * q) << 16);
     const int nln = (3 * nkb + 7) / 8;
@@ -577,28 +591,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int sp = (int)((wg - step0) & 3);
       const int f = sp;                        // first own step: sp % 4 for all of them
       const uint32_t g0 = line0 + (6 * f >> 3), g1 = g0 + 1;
-      const uint32_t s0 = g0 % SC, s1 = g1 % SC;
-      uint32_t ph0 = (g0 / SC) & 1, ph1 = (g1 / SC) & 1;
+      int s0 = (int)(g0 % a.sc), s1 = (int)(g1 % a.sc);
+      uint32_t ph0 = (g0 / a.sc) & 1, ph1 = (g1 / a.sc) & 1;
       const bool two = f == 1 || f == 2;       // the step's chunks end in the next line
-      uint32_t at[6];
+      uint32_t at[6];                          // the chunks' places in their line
 #pragma unroll
-      for (int j = 0; j < 6; ++j) {
-        const int c = 6 * f + j;
-        at[j] = crow + ((c >> 3) == (6 * f >> 3) ? s0 : s1) * C_BYTES + (((c ^ row) & 7) << 4);
-      }
+      for (int j = 0; j < 6; ++j) at[j] = crow + ((((6 * f + j) ^ row) & 7) << 4);
+      const int in0 = 8 - (6 * f & 7);         // chunks of the step in its first line
       for (; sp < nst; sp += 4) {
         const bool half = 2 * sp + 1 == nkb, last = sp + 1 == nst;   // half: a last step of one K block
         const bool next = two && !(half && f == 2);
         if (!warp_wait(bar.full_c + 8 * s0, ph0, 0) || (next && !warp_wait(bar.full_c + 8 * s1, ph1, 0))) { ok = false; break; }
-        ph0 ^= 1;
-        ph1 ^= 1;
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
           if (b == 1 && half) break;
           uint32_t w[12], out[32];
 #pragma unroll
           for (int j = 0; j < 3; ++j)
-            lds128(b ? at[3 + j] : at[j], w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            lds128((b ? at[3 + j] : at[j]) + (3 * b + j < in0 ? s0 : s1) * C_BYTES, w[4 * j], w[4 * j + 1], w[4 * j + 2],
+                   w[4 * j + 3]);
           if (b == 1 || half) {
             // The codes are in registers (the arrival is ordered after the warp's loads): the lines go back before the
             // lookups.  A line belongs to two steps, or to the tile's last one alone, which then arrives twice.
@@ -620,6 +631,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         sm100::tc_fence_before();
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive_cluster_relaxed(ready + 8 * sa);
+        if ((s0 += 3) >= a.sc) {               // three lines on (a.sc >= 3)
+          s0 -= a.sc;
+          ph0 ^= 1;
+        }
+        if ((s1 += 3) >= a.sc) {
+          s1 -= a.sc;
+          ph1 ^= 1;
+        }
         sa += 4;                               // four steps on (a.sa >= 4)
         if (sa >= a.sa) {
           sa -= a.sa;
@@ -826,7 +845,7 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
   CUtensorMap mc, mc2;
   if (!codes_map(&mc, codes) || !codes_map(&mc2, codes2 ? codes2 : codes))
     return fail(QL_ERR_CUDA, "%s: cannot encode the code tensor map", who);
-  Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), 0, 0, 0, 0, 0, ydt == QL_OUT_BF16 && N % 8 == 0, K, 1};
+  Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), 0, 0, 0, 0, 0, 0, ydt == QL_OUT_BF16 && N % 8 == 0, K, 1};
   // Positions per tile: room for a group of four times the average length, so that few groups take a second pass
   // over their codes, and no more than that: what accumulators and x rows do not take is more stages.  (4096 tokens of
   // a 64-expert layer, 512 rows per expert: gate/up 1.26 ms with 128, 0.95 with 256; 256 tokens: 0.276 with 64, 0.239
@@ -845,7 +864,11 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
   // one of the stage's earlier uses are over, so the phase's parity tells the one that it waits for.
   a.sa = std::min(SA_MAX, (512 - 2 * a.slot) / 64);
   a.xr = room(a.nt_max) / 2;
-  a.xst = std::min(SX_MAX, X_RING / (2 * a.xr * 128));
+  const int stage = 2 * a.xr * 128;
+  a.xst = std::min(SX_MAX, (XC_RING - SC_MIN * C_BYTES) / stage);
+  if (a.xr == 64) a.xst = 4;
+  static_assert((XC_RING - SC_MIN * C_BYTES) / (NT * 128) >= XPARTS);
+  a.sc = std::min(SC_MAX, (XC_RING - a.xst * stage) / C_BYTES);
   // the most tiles that the counts could make (each group may end inside a tile)
   const int64_t items = ((int64_t)std::min(g.G, g.M) + g.M / a.nt_max) * a.ntl;
   auto go = [&](auto gated) -> ql_status {

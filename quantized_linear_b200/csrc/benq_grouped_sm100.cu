@@ -71,6 +71,9 @@ constexpr int NBAR = 2 * SX_MAX + 2 * SA_MAX + 2 * SC_MAX + 8;
 constexpr int OFF_MISC = NBAR * 8;             // tensor-memory address, abort flag
 constexpr int OFF_GRP = OFF_MISC + 16;         // token tiles before each group, int [G + 1]
 constexpr int OFF_Y1 = (OFF_GRP + (QL_MAX_GROUPS + 1) * 4 + 15) / 16 * 16;   // the second half's output rows (see OFF_YROW)
+constexpr int TILES = 16;                      // tiles listed ahead: warp 2 is at most 2 tiles before the decoders, they at most
+                                               // SA_MAX (of one step each) before the MMAs, those 2 before the epilogue
+constexpr int OFF_TILE = OFF_Y1 + 4 * (NT / 2) * 4;   // 16 bytes each
 constexpr int OFF_X = 2 * TBL_BYTES;           // from the tables on
 constexpr int STG_BYTES = 1024;                // per epilogue warp: 16 positions x 32 features of bf16
 constexpr int OFF_STG = OFF_X + XC_RING;
@@ -78,7 +81,7 @@ constexpr int OFF_ROW = OFF_STG + 4 * STG_BYTES;      // in place of the second 
                                                       // gathers, int [NT / 2]
 constexpr int OFF_YROW = OFF_STG + 8 * STG_BYTES;     // per quarter of tensor memory: the output rows of a tile's first half, int [NT / 2]
 constexpr int SMEM_BYTES = FRONT + OFF_YROW + 4 * (NT / 2) * 4;
-static_assert(OFF_Y1 + 4 * (NT / 2) * 4 <= FRONT, "front");
+static_assert(TILES > 2 + SA_MAX + 2 && OFF_TILE + TILES * 16 <= FRONT, "front");
 static_assert(D_MAX + 64 * 4 <= 512, "tensor memory: four stages of decoded W beside the accumulators");
 static_assert(OFF_X % 1024 == 0 && C_BYTES % 1024 == 0 && OFF_STG % 128 == 0, "alignment");
 static_assert(2 * XPARTS * (NT / 2) * 4 <= 4 * STG_BYTES && SMEM_BYTES <= 232448, "shared memory");
@@ -255,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t rank = sm100::cluster_ctarank();
   const bool lead = rank == 0;
   const Wait wt{tmem_slot + 4, sm100::mapa_shared(tmem_slot + 4, rank ^ 1u)};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // known to be uniform
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int nkb = a.K / 64, nst = (nkb + 1) / 2;   // K blocks, steps
   const uint32_t xblk = a.xr * 128;                // bytes of a 64-column block of an x stage
@@ -288,6 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       sm100::mbar_init(bar.acc_empty + 8 * s, 2 * 4 * sets);
     }
     sts32(tmem_slot + 4, 0);
+    for (int i = 0; i < TILES; ++i) sts32(raw + OFF_TILE + 16 * i, 0xffffffffu);
     sm100::fence_barrier_init();
     sm100::prefetch_tensormap(&map_x);
     sm100::prefetch_tensormap(&map_c);
@@ -327,24 +331,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t a_col = tmem + 2 * a.slot;        // the stages of decoded W
   // (a plan whose groups overlap can have more tiles than any real one: the count stays within 31 bits)
   const int nitems = (int)min((int64_t)cum[G] * a.ntl, (int64_t)1 << 30);
-  auto tile_at = [&](int item) {
+  // A tile's place and length take two searches' worth of shared and global latency: warp 2, which is ahead of the others,
+  // works them out and lists them, numbered.
+  auto tile_at = [&](int item) {               // by a whole warp
     Tile t;
     const int tt = item / a.ntl;
     t.wt = item - tt * a.ntl;
-    int lo = 0, hi = G - 1;   // the group with cum[g] <= tt < cum[g + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid + 1] <= tt) lo = mid + 1; else hi = mid;
-    }
-    t.g = lo;
-    const int s0 = max(0, min(a.g.M, __ldcg(a.g.offsets + lo))), s1 = max(0, min(a.g.M, __ldcg(a.g.offsets + lo + 1)));
-    const int nt = cum[lo + 1] - cum[lo], per = min(a.nt_max, (s1 - s0 + nt - 1) / nt);   // a group's tiles are of equal length
-    t.p0 = s0 + (tt - cum[lo]) * per;
-    t.p1 = min(s1, t.p0 + per);
+    // the group with cum[g] <= tt < cum[g + 1]: first its 32, then itself
+    const unsigned past = __ballot_sync(0xffffffffu, 32 * (lane + 1) < G && cum[min(32 * (lane + 1), G)] <= tt);
+    const int g32 = 32 * __popc(past);
+    t.g = g32 + __popc(__ballot_sync(0xffffffffu, g32 + lane + 1 < G && cum[min(g32 + lane + 1, G)] <= tt));
+    const int s0 = max(0, min(a.g.M, __ldcg(a.g.offsets + t.g))), s1 = max(0, min(a.g.M, __ldcg(a.g.offsets + t.g + 1)));
+    const int nt = cum[t.g + 1] - cum[t.g];
+    const int per = min(a.nt_max, (s1 - s0 + nt - 1) / nt);   // a group's tiles are of equal length
+    t.p0 = s0 + (tt - cum[t.g]) * per;
+    t.p1 = max(t.p0, min(s1, t.p0 + per));
     const int n = (per + 15) & ~15;
     t.halves = n > a.slot ? 2 : 1;
     t.nh = t.halves == 2 ? ((n / 2 + 15) & ~15) : n;
     return t;
+  };
+  const uint32_t tiles = raw + OFF_TILE;
+  auto list_tile = [&](int number, int item, const Tile &t) {
+    if (lane == 0)
+      sts128v(tiles + (number % TILES) * 16, (uint32_t)item, (uint32_t)t.p0, (uint32_t)t.wt,
+              (uint32_t)(t.g | (t.nh << 10) | (t.halves << 18) | ((t.p1 - t.p0) << 20)));
+  };
+  auto listed_tile = [&](int number, int item, Tile &t) {   // by any threads; false: gave up
+    const uint32_t from = tiles + (number % TILES) * 16;
+    uint32_t x, p0, wt_, w;
+    lds128(from, x, p0, wt_, w);
+    if (x != (uint32_t)item) {
+      const long long t0 = clock64();
+      do {
+        __nanosleep(NAP);
+        if (ld_volatile_u32(wt.abort_local) != 0 || clock64() - t0 > WAIT_BUDGET) return false;
+        lds128(from, x, p0, wt_, w);
+      } while (x != (uint32_t)item);
+    }
+    t.p0 = (int)p0;
+    t.wt = (int)wt_;
+    t.g = (int)(w & 1023);
+    t.nh = (int)(w >> 10 & 255);
+    t.halves = (int)(w >> 18 & 3);
+    t.p1 = t.p0 + (int)(w >> 20);
+    return true;
   };
 
   if (warp == 0 || warp == 3 || (warp >= 8 + NDW && gathered)) {
@@ -355,10 +386,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // needs 1100 clocks for a step however few its rows, most of them behind the decoders' lookups.  (As with decoded W, a
     // phase's parity tells enough as long as there are no fewer stages than turns.)
     const int xi = warp == 0 ? 0 : warp == 3 ? 1 : warp - (8 + NDW) + 2, b = xi & 1, parts = gathered ? XPARTS : 1;
-    int turn = xi >> 1;                        // steps until this warp's next
+    int turn = xi >> 1, tl = 0;                // steps until this warp's next, tiles
     uint32_t ph = 1;                           // a fresh barrier passes a wait for the phase before its first
-    for (int wi = pair; wi < nitems && ok; wi += npairs) {
-      const Tile t = tile_at(wi);
+    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
+      Tile t;
+      if (!__all_sync(0xffffffffu, listed_tile(tl, wi, t))) { ok = false; break; }
       const int nr = t.nh / 2;                 // rows of this CTA per half
       const int boxes = (nr + X_BOX - 1) / X_BOX;
       const int rows = gathered ? nr : boxes * X_BOX;   // rows copied per half
@@ -423,13 +455,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // One lane does it all.  A look at a barrier takes 180 clocks behind the decoders' lookups even when its phase has
     // long completed, so the next step's two are looked at before this step's MMAs are issued.
     if (lead && sm100::elect_one()) {
-      int sx = 0, sa = 0;
+      int sx = 0, sa = 0, tl = 0;
       uint32_t phx = 0, pha = 0;
       bool seen = false;                       // the coming step's x and W are there
       Slots sl;
       const uint64_t xdesc = sm100::sw128_kmajor_desc(sbase + OFF_X);   // + address / 16 (below 2^14: no carry)
-      for (int wi = pair; wi < nitems && ok; wi += npairs) {
-        const Tile t = tile_at(wi);
+      for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
+        Tile t;
+        if (!listed_tile(tl, wi, t)) { ok = false; break; }
         const int slots = a.nseg > 1 ? 2 : t.halves, first_slot = sl.take(slots);
         // a tile of two slots waits for the second one when its first step has multiplied into the first
         const bool wait1 = first_slot + slots == 2 && sl.used1 > 0, late1 = t.halves == 2;
@@ -528,6 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     };
     if (pair < nitems) {                       // the first tile's tables
       nx = tile_at(pair);
+      list_tile(0, pair, nx);
       q = 0;
       load();
       while (q < 4) store(0);
@@ -539,6 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int b = (tl + 1) & 1;              // the next tile's table buffer
       if (wi + npairs < nitems) {
         nx = tile_at(wi + npairs);
+        list_tile(tl + 1, wi + npairs, nx);
         q = 0;
         load();
       }
@@ -656,8 +691,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int q = warp & 3, c0 = warp >= 8 ? 16 : 0, cstep = 16 * sets;   // this warp's lanes of tensor memory, its chunks
     const uint32_t lead_empty = sm100::mapa_shared(bar.acc_empty, 0);
     Slots sl;
-    for (int wi = pair; wi < nitems && ok; wi += npairs) {
-      const Tile t = tile_at(wi);
+    int tl = 0;
+    for (int wi = pair; wi < nitems && ok; wi += npairs, ++tl) {
+      Tile t;
+      if (!__all_sync(0xffffffffu, listed_tile(tl, wi, t))) { ok = false; break; }
       const bool runs = a.nseg > 1;            // both slots hold one tile's runs
       const int slots = runs ? 2 : t.halves, first_slot = sl.take(slots), used0 = sl.used0, used1 = sl.used1;
       sl.done(first_slot, slots);

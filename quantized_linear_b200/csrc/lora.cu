@@ -428,10 +428,19 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
 // Whether the tiles of 64 positions fill: 16 rows per adapter on average, or more.
 bool many_rows(int G, int T) { return T / std::min(G, T) >= 16; }
 
+// Whether the shrink takes its ring form: tiles of 64 positions that fill, or 64 adapters (times layers) with more than 16
+// ranks, whose copies then keep more in flight than loads to registers do.  (64 adapters of rank 32, K = 5120, plan and
+// expand included: 130 rows 36 us, 34 with the ring; 500 rows 47, 39.  32 adapters of rank 16 for q, k and v: 200 rows 28,
+// 36 with the ring.)
+bool takes_ring(int S, int G, int T, int r, int K) {
+  const int groups = std::min(G, T);
+  return K % 8 == 0 && (many_rows(G, T) || (T / groups >= 2 && r > 16 && groups * S >= 64));
+}
+
 // CTAs that share K: enough that the shrink tiles of an ordinary batch fill the SMs, each with a few blocks of inputs per
 // warp.  (Depends on the call's sizes alone, so that results do.)
-int k_shares(int S, int G, int T, int K) {
-  const bool ring = many_rows(G, T) && K % 8 == 0;
+int k_shares(int S, int G, int T, int r, int K) {
+  const bool ring = takes_ring(S, G, T, r, K);
   const int64_t tiles = ((int64_t)std::min(G, T) + T / (ring ? RT : ST)) * S;
   const int64_t want = std::max<int64_t>(1, 2 * 148 / std::max<int64_t>(1, tiles));
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, KS_MAX, K / (ring ? RK * 8 : 32 * WARPS * 4)}));
@@ -446,14 +455,15 @@ size_t lora_workspace_size(int S, int T, int r) { return ((size_t)KS_MAX * S * T
 ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, const int32_t *order,
                           const int32_t *offsets, const float *scale, ql_out_dtype ydt, int G, int T, int r, int K,
                           void *ws, cudaStream_t s) {
-  const bool many = many_rows(G, T), ring = many && K % 8 == 0;
-  // feature rounds per expand CTA, which prepares t once for them: two CTAs per SM in all; t of 16 positions is little,
-  // and more CTAs in flight count for more (q, k, v of 32 rows: 6.6 us, 8.6 with two rounds)
+  const bool many = many_rows(G, T), ring = takes_ring(S, G, T, r, K);
+  // feature rounds per expand CTA, which prepares t once for them: as many as leave two CTAs per SM, three of the small
+  // tiles (q, k, v of 32 rows: 6.6 us with one round, 8.6 with two; 500 rows of 64 adapters: 22.0 with one, 20.1 with four)
   const int et = many ? (ydt == QL_OUT_F32 ? 32 : 64) : 16;
   int64_t all = 0;
   for (int i = 0; i < S; ++i) all += (layers[i].N + EF - 1) / EF;
   all *= std::min(G, T) + T / et;
-  const int rounds = !many ? 1 : (int)std::max<int64_t>(1, (all + 2 * sm_count() - 1) / (2 * sm_count()));
+  const int rounds =
+      (int)std::max<int64_t>(1, many ? (all + 2 * sm_count() - 1) / (2 * sm_count()) : all / (3 * sm_count()));
   Layers L{};
   for (int i = 0; i < S; ++i) {
     L.A[i] = layers[i].A;
@@ -463,7 +473,7 @@ ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, co
     L.chunk0[i + 1] = L.chunk0[i] + (layers[i].N + EF * rounds - 1) / (EF * rounds);
   }
   float *t = static_cast<float *>(ws);
-  const int shares = k_shares(S, G, T, K);
+  const int shares = k_shares(S, G, T, r, K);
   auto tiles = [&](int tt) { return (unsigned)(std::min(G, T) + T / tt); };   // the most that the counts could make
   auto shrink = [&](auto kern, int tile, size_t smem) -> bool {
     if (smem > 40 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;

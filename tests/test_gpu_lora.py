@@ -55,6 +55,8 @@ CASES = [
     # many rows per adapter, features in whole strips of 32
     (400, 3, 64, 192, (544, 96)), (300, 2, 24, 128, (288,)), (500, 4, 128, 256, (1056,)), (700, 1, 8, 64, (64, 32, 32, 96)),
     (129, 1, 72, 72, (2080,)), (1000, 5, 40, 320, (512, 256)),
+    # many adapters of a few rows
+    (150, 70, 40, 136, (200,)), (300, 64, 33, 264, (96, 40)), (300, 100, 20, 64, (5120,)),
 ]
 
 

@@ -408,8 +408,8 @@ QL_API ql_status moe_combine(const void *y, ql_out_dtype y_dtype, const int32_t 
  *   the rows i = order[p] of adapter g (offsets[g] <= p < offsets[g + 1]),
  *     y_s[i][n] += scale[g] * sum_j B_s[g][n][j] * ( sum_k A_s[g][j][k] * x[i][k] ).
  *   The projection (benq_linear, mdbf_linear, ...) has written y_s before; rows of no adapter keep
- *   it.  The inner sums are fp32 and enter the second product as a bf16 pair hi + lo (2^-17
- *   relative); an fp32 y takes one rounding of the sum, a bf16 y one rounding to nearest even.
+ *   it.  The inner sums are fp32 and enter the second product as a sum of bf16 terms, two for a bf16 y
+ *   (2^-17 relative), three for an fp32 y (2^-25); y takes one rounding of the sum, to nearest even.
  *   layers   host array of S entries (1 <= S <= 4) that read the same x; no two with one y.
  *   x        device bf16 bits [T][K]; order device int32 [T], offsets device int32 [G + 1]: the plan
  *            of the rows' adapters (no row twice).

@@ -7,8 +7,8 @@
 //           eight; the warps of a CTA and up to KS_MAX CTAs share out K.  Few rows per adapter: tiles of 32 positions,
 //           fragments loaded straight from memory.  Many: tiles of 64, through a ring of asynchronous copies;
 //   expand  y += B t, tiles of 16 to 64 positions by strips of 32 features per warp: t, summed over the K shares in
-//           order, scaled and split into a bf16 pair hi + lo (2^-17 relative), is the MMA's A from shared memory,
-//           B's rows its N.
+//           order, scaled and split into bf16 terms (lora::parts: 2^-17 relative for a bf16 y, 2^-25 for fp32), is the
+//           MMA's A from shared memory, B's rows its N.
 // Both are bound by memory: A and B of the adapters in use, and y read and written, which outweighs all else
 // when a tile is full.  The K index of a fragment is permuted (the same way on both sides), so that a lane's
 // elements are consecutive in memory: 16-byte loads of A and x, 8-byte loads of B.  The four 8-feature MMA
@@ -275,8 +275,8 @@ template <bool F32, int MTL>
 __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
     lora_expand_kernel(const Layers L, int S, const int32_t *order, const int32_t *offsets, const float *scale, int G,
                        int T, int r, int shares, int rounds, const float *t) {
-  constexpr int ET = 16 * MTL, KC = MTL == 1 ? 4 : 1;
-  extern __shared__ __align__(16) unsigned char esm[];   // t as bf16: [hi, lo][ET][rp], rows of rp * 2 bytes
+  constexpr int ET = 16 * MTL, KC = MTL == 1 ? 4 : 1, PARTS = lora::parts(F32);
+  extern __shared__ __align__(16) unsigned char esm[];   // t as bf16: [PARTS][ET][rp], rows of rp * 2 bytes
   __shared__ int where[3], rows[ET];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int tile = blockIdx.x / L.chunk0[S], chunk = blockIdx.x - tile * L.chunk0[S];
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
   const int mt = MTL == 1 ? 1 : (count + 15) / 16;
   const bool vec = r % 4 == 0;                    // 8-byte aligned rows of B
   const bool whole = N % 8 == 0;                  // 16-byte aligned pieces of y, none partial
-  uint16_t *hi = reinterpret_cast<uint16_t *>(esm), *lo = hi + ET * rp;
+  uint16_t *const tp = reinterpret_cast<uint16_t *>(esm);
   // MMA column c of the strip's tile i is feature n0 + 8 (c / 2) + 2 i + c % 2
   uint2 b[KC][4];
   auto load_b = [&](int n0, int k0) {
@@ -343,15 +343,15 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
       for (int z = 0; z < shares; ++z) v += __ldcg(src + (int64_t)z * S * T * r);
       v *= f;
     }
-    const uint16_t h = qld::f32_to_bf16_rn(v);
-    const float rest = v - qld::bf16_to_f32(h);
     // place of rank index j within its 16: lane (j % 16) / 4 takes elements j % 4 as fragment columns 2 tig, 2 tig + 8
     const int e = j & 3, at = (j & ~15) + 2 * ((j & 15) >> 2) + (e & 1) + 8 * (e >> 1);
-    hi[p * rp + at] = h;
-    lo[p * rp + at] = (rest == rest) ? qld::f32_to_bf16_rn(rest) : 0;   // inf and NaN are in hi alone
+    uint16_t part[PARTS];
+    lora::split(v, part);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) tp[(q * ET + p) * rp + at] = part[q];
   }
   __syncthreads();
-  const uint32_t frag = static_cast<uint32_t>(__cvta_generic_to_shared(hi)) + ((lane & 15) * rp + (lane >> 4) * 8) * 2;
+  const uint32_t frag = static_cast<uint32_t>(__cvta_generic_to_shared(tp)) + ((lane & 15) * rp + (lane >> 4) * 8) * 2;
   for (int rd = 0; rd < rounds; ++rd) {
     const int n0 = f0 + rd * EF + 32 * warp, n = n0 + 8 * tig;
     if (f0 + rd * EF >= N) break;
@@ -367,13 +367,12 @@ __global__ void __launch_bounds__(WARPS * 32, MTL == 1 ? 3 : 2)
 #pragma unroll
         for (int m = 0; m < MTL; ++m)
           if (m < mt) {
-            uint32_t ah[4], al[4];
-            ldmatrix_x4(frag + (16 * m * rp + 16 * (k0 + k)) * 2, ah);
-            ldmatrix_x4(frag + ((ET + 16 * m) * rp + 16 * (k0 + k)) * 2, al);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              mma16816(acc[m][i], al[0], al[1], al[2], al[3], b[k][i].x, b[k][i].y);
-              mma16816(acc[m][i], ah[0], ah[1], ah[2], ah[3], b[k][i].x, b[k][i].y);
+            for (int q = PARTS - 1; q >= 0; --q) {   // the smallest first
+              uint32_t v[4];
+              ldmatrix_x4(frag + ((q * ET + 16 * m) * rp + 16 * (k0 + k)) * 2, v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma16816(acc[m][i], v[0], v[1], v[2], v[3], b[k][i].x, b[k][i].y);
             }
           }
       }
@@ -496,7 +495,7 @@ ql_status lora_add_launch(const lora_layer *layers, int S, const uint16_t *x, co
   auto expand = [&](auto f32c, auto mtl) -> bool {
     constexpr int ET = 16 * decltype(mtl)::value;
     auto kern = lora_expand_kernel<decltype(f32c)::value, decltype(mtl)::value>;
-    const size_t smem = (size_t)2 * ET * ((r + 15) / 16 * 16 + 8) * 2;
+    const size_t smem = (size_t)lora::parts(decltype(f32c)::value) * ET * ((r + 15) / 16 * 16 + 8) * 2;
     if (smem > 40 * 1024 && set_max_smem(kern, (int)smem) != cudaSuccess) return false;
     launch(kern, dim3(L.chunk0[S] * tiles(ET)), WARPS * 32, smem, s, L, S, order, offsets, scale, G, T, r, shares, rounds,
            static_cast<const float *>(t));

@@ -14,6 +14,20 @@ struct Layers {
   int chunk0[MAX_LAYERS + 1];        // expand: feature chunks (or runs of them) before each layer
 };
 
+// The inner sums enter the second product as a sum of bf16 terms: two leave 2^-17 of a value, below the rounding of a bf16
+// y; an fp32 y takes three (2^-25).
+constexpr int parts(bool f32) { return f32 ? 3 : 2; }
+
+template <int P>
+__device__ __forceinline__ void split(float v, uint16_t (&part)[P]) {
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    part[q] = qld::f32_to_bf16_rn(v);
+    v -= qld::bf16_to_f32(part[q]);
+    if (v != v) v = 0.f;                       // inf and NaN are in the first term alone
+  }
+}
+
 // The tile'th tile of `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
 // Returns the number of tiles before the group that it stopped at (with tile past the last: the number of all tiles).
 __device__ __forceinline__ int find_tile(const int32_t *offsets, int G, int T, int tt, int tile, int &g, int &p0, int &p1) {

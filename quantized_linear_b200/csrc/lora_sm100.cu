@@ -2,12 +2,12 @@
 //   y[i][n] += sum_j B_g[n][j] t[i][j] for 128 positions of one adapter by 256 features at a time.
 //
 // What it cannot do without is y, read and written once (4 bytes per output in bf16).  On the warp MMA the products of
-// the pair t = hi + lo alone take as long as that traffic (447 TFLOP/s measured) and their operands' loads longer;
+// t's bf16 terms alone take as long as that traffic (447 TFLOP/s measured) and their operands' loads longer;
 // here they cost the issuing threads nothing.  A CTA (17 warps, one per SM) walks a run of
 // (layer, tile, 256 features) units, runs of equal length over the actual tiles:
 //   * warp 16 loads B's rows by tensor copies (two stages) and issues the MMAs, a unit ahead: M = 128 positions,
-//     N = 256 features, K = r twice (hi, then lo, against the same B), into two accumulators of 256 columns;
-//   * warps 0-15 prepare t when the tile changes (sum of the K shares in order, scale, hi + lo, 128-byte swizzled rows), request
+//     N = 256 features, K = r for each term of t against the same B, into two accumulators of 256 columns;
+//   * warps 0-15 prepare t when the tile changes (sum of the K shares in order, scale, bf16 terms, 128-byte swizzled rows), request
 //     the unit's y values, and add the accumulators to them.
 // The copy's five dimensions (k, feature bit 0, bits 3-4, bits 1-2, the rest) permute the features of each 32 so that
 // a lane's accumulator fragments (tcgen05.ld 16x256b: two columns of each eight) are 8 consecutive features: 16-byte
@@ -60,15 +60,16 @@ template <bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     lora_expand_mma_kernel(const __grid_constant__ Maps maps, const Layers L, int S, const int32_t *order,
                            const int32_t *offsets, const float *scale, int G, int T, int r, int shares, const float *t) {
+  constexpr int PARTS = lora::parts(F32);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ int rows[TM], where[4];
   __shared__ __align__(8) uint64_t bars[2 * BST + 6];
   __shared__ uint32_t tmem_word, abort_word;
   const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
-  const uint32_t tb = (raw + 1023u) & ~1023u;            // t: [hi, lo][64-wide block][128 rows x 128 bytes]
+  const uint32_t tb = (raw + 1023u) & ~1023u;            // t: [PARTS][64-wide block][128 rows x 128 bytes]
   const int kch = (r + 63) / 64;
   const uint32_t bbytes = kch * TN * 128;
-  const uint32_t bb = tb + 2 * kch * TM * 128;           // B: [stage][block][256 rows x 128 bytes]
+  const uint32_t bb = tb + PARTS * kch * TM * 128;           // B: [stage][block][256 rows x 128 bytes]
   const uint32_t b_full = static_cast<uint32_t>(__cvta_generic_to_shared(bars)), b_free = b_full + 8 * BST;
   const uint32_t d_full = b_free + 8 * BST, d_free = d_full + 16, t_full = d_free + 16, meet = t_full + 8;
   const uint32_t tslot = static_cast<uint32_t>(__cvta_generic_to_shared(&tmem_word));
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       sm100::tc_fence_after();
       if (sm100::elect_one()) {
         uint32_t add = 0;
-        for (int h = 1; h >= 0; --h)                     // lo first
+        for (int h = PARTS - 1; h >= 0; --h)             // the smallest terms first
           for (int b = 0; b < kch; ++b) {
             const uint64_t ad = sm100::sw128_kmajor_desc(tb + (h * kch + b) * TM * 128);
             const uint64_t bd = sm100::sw128_kmajor_desc(bb + st * bbytes + b * TN * 128);
@@ -229,16 +230,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           const float e[4] = {a.x * f, a.y * f, a.z * f, a.w * f};
-          uint32_t hi[4], lo[4];
+          uint16_t term[4][PARTS];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            hi[x] = qld::f32_to_bf16_rn(e[x]);
-            const float rest = e[x] - qld::bf16_to_f32(hi[x]);
-            lo[x] = rest == rest ? qld::f32_to_bf16_rn(rest) : 0;   // inf and NaN are in hi alone
-          }
+          for (int x = 0; x < 4; ++x) lora::split(e[x], term[x]);
           const uint32_t at = tb + (j >> 6) * TM * 128 + p * 128 + ((((j & 63) >> 3) ^ (p & 7)) << 4) + (j & 7) * 2;
-          sts64(at, hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          sts64(at + kch * TM * 128, lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+            sts64(at + h * kch * TM * 128, term[0][h] | ((uint32_t)term[1][h] << 16), term[2][h] | ((uint32_t)term[3][h] << 16));
         }
         sm100::fence_proxy_async_smem();
         __syncwarp();
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-size_t smem_bytes(int r) { return (size_t)((r + 63) / 64) * (2 * TM + BST * TN) * 128 + 1024; }
+size_t smem_bytes(int r, bool f32) { return (size_t)((r + 63) / 64) * (lora::parts(f32) * TM + BST * TN) * 128 + 1024; }
 
 }  // namespace
 
@@ -354,7 +352,7 @@ ql_status expand_mma_launch(const Layers &in, int S, const int32_t *order, const
   }
   units = ((int64_t)std::min(G, T) + T / TM) * L.chunk0[S];
   const int grid = (int)std::min<int64_t>(units, ql::sm_count());
-  const size_t smem = smem_bytes(r);
+  const size_t smem = smem_bytes(r, ydt == QL_OUT_F32);
   auto go = [&](auto kern) -> ql_status {
     if (ql::set_max_smem(kern, (int)smem) != cudaSuccess) return ql::fail(QL_ERR_CUDA, "lora_add: cannot reserve shared memory");
     ql::launch(kern, grid, THREADS, smem, s, maps, L, S, order, offsets, scale, G, T, r, shares, t);

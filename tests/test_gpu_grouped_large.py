@@ -100,4 +100,4 @@ def test_lora_past_32_bits(ql, T, G, N, r, K, dtype):
     for i, t in enumerate(pick.tolist()):
         a, b, v = A[index[t]].double(), B[index[t]].double(), x[t].double()
         ref, s = y0[i] + b @ (a @ v), b.abs() @ (a.abs() @ v.abs())
-        _near(y[t], ref, ((K / 8 + 64 + r + 8) * 2.0 ** -23 + 2.0 ** -17) * s, dtype)
+        _near(y[t], ref, ((K / 8 + 64 + r + 8) * 2.0 ** -23 + (2.0 ** -17 if dtype == torch.bfloat16 else 2.0 ** -25)) * s, dtype)

@@ -1,8 +1,9 @@
 """Low-rank adapters of many requests on the GPU against oracle/grouped.py (fp64).
 
 Tolerance, per element, with s = |scale| |B| (|A| |x|): the inner sum takes at most K/8 + 64 fp32
-roundings of 2^-23 on its way (plain or tensor-core adds), the bf16 pair that enters the second product
-2^-17, the outer sum r + 8 more, so |error| <= ((K/8 + 64 + r + 8) 2^-23 + 2^-17) s; then the addition to
+roundings of 2^-23 on its way (plain or tensor-core adds), the bf16 terms that enter the second product leave
+2^-17 (two, for a bf16 y) or 2^-25 (three, for fp32), the outer sum r + 8 more, so
+|error| <= ((K/8 + 64 + r + 8) 2^-23 + 2^-17 or 2^-25) s; then the addition to
 y: 2^-24 of the result in fp32, 2^-8 in bf16.
 """
 import numpy as np
@@ -38,7 +39,7 @@ def _bits(rng, *shape, f=1.0):
 
 def _check(got, y0, A, B, xb, index, scale, K, r, dtype):
     ref, s = og.lora(A, B, y0, xb, index, scale)
-    bound = ((K / 8 + 64 + r + 8) * 2.0 ** -23 + 2.0 ** -17) * s
+    bound = ((K / 8 + 64 + r + 8) * 2.0 ** -23 + (2.0 ** -17 if dtype == torch.bfloat16 else 2.0 ** -25)) * s
     bound = bound + (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24) * (np.abs(ref) + bound) + 1e-37
     none = (np.asarray(index) < 0) | (np.asarray(index) >= A.shape[0])
     bound[none] = 0                                          # rows of no adapter keep their bits

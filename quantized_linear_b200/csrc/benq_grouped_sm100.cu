@@ -15,20 +15,23 @@
 // Per 64-wide K block and SM that is 256 + 48 wavefronts of lookups and codes, 48 of code writes and
 // n/2 + n/2 of X for n positions, against 2 n clocks of MMA.
 //
-// Roles (896 threads per CTA), in steps of two K blocks: warps 0, 3 and 24-27 load X, half of them each K block (rows
-// gathered by x_rows, four to a copy that takes 50 clocks to issue, or tiles); warp 1 issues the MMAs (even CTA);
-// warp 2 loads codes and, between them, lays out the next tile's tables; warps 4-7 drain the accumulators; warps 8-23
-// are four warpgroups of decoders, each taking every fourth step.  Accumulators are two slots, so that one tile's
-// epilogue overlaps the next tile's MMAs.  The decoders of the odd CTA arrive at the even CTA's barrier with relaxed
+// Roles (896 threads per CTA), in steps of two K blocks: warps 0, 3 and 24-27 load X, a pair per step in turn, a K block
+// each (rows gathered by x_rows, four to a copy that takes 50 clocks to issue; where nothing is gathered, warps 0 and 3
+// load tiles and 24-27 are a second set of epilogue warps); one lane of warp 1 issues the MMAs (even CTA); warp 2 loads
+// codes, lays out the next tile's tables between them and lists the tiles for the others; warps 4-7 drain the
+// accumulators; warps 8-23 are four warpgroups of decoders, each taking every fourth step.  Accumulators are two slots, so
+// that one tile's epilogue overlaps the next tile's MMAs.  The decoders of the odd CTA arrive at the even CTA's barrier with relaxed
 // semantics: what they hand over is in tensor memory, which the tcgen05 fences order (a cluster-scope release by one
 // relaying thread took 1300 clocks per K block and set the kernel's pace).
 //
 // Measured for a K block of 2 x 128 rows: lookups alone 311 clocks (16 warps, with the stores to tensor memory); the
-// kernel takes about 580 with few positions, where the decoders' waits and the polling of the other warps share the
-// issue slots with the lookups, and about 950 with 256 gathered positions.
+// kernel takes about 480 with few positions, where the lane that issues the MMAs shares its scheduler with the decoders
+// (issue slots 76 % busy), and about 1000 with 256 gathered positions, whose copies take 8 clocks per row.  64 tokens
+// through 64 experts (K 5120, N 1088, gated): 166 us, 4096 tokens 830 us.
 //
-// The gated form gives each warp of lanes 16 gate rows and the same features' 16 up rows: silu(g) * u then needs
-// one exchange between the halves of a warp.
+// The gated form gives each warp of lanes 16 gate rows and the same features' 16 up rows: silu(g) * u then needs no
+// exchange where bf16 leaves in 16-byte pieces (a fragment load of either half has the same features and positions), and one
+// between the halves of the warp otherwise.
 //
 // The tensor core adds to its fp32 accumulator with truncation, about K * 1e-9 of the result after K
 // inputs.  That is far below a bf16 rounding; for fp32 outputs each run of `seg` steps (512 inputs, more only
@@ -57,7 +60,7 @@ constexpr int X_BOX = 32;                      // rows per copy when rows are no
 constexpr int C_LINE = 128;                    // code bytes per row and stage: 128-byte rows in the 128-byte swizzle.  (Unswizzled
 constexpr int C_BYTES = RW * C_LINE;           // 144-byte rows, three K blocks, took the TMA unit 21 clocks each.)  16 KB
 constexpr int TBL_BYTES = 4 * 8192;            // lane-private tables: 4 warps of rows x [64][32] words, two buffers
-constexpr int NDW = 16;                        // decoder warps: four warpgroups, two per step in turn
+constexpr int NDW = 16;                        // decoder warps: four warpgroups, one per step in turn
 constexpr int XPARTS = 3;                      // pairs of warps that gather x rows, a step each in turn
 constexpr int THREADS = (8 + NDW + 2 * (XPARTS - 1)) * 32;
 constexpr int D_MAX = 256;                     // tensor memory columns: at most these are accumulators, then steps of 2 x 32
@@ -885,8 +888,8 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
   Args a{lut, lut2, g, y, (int)ydt, N, K, (N + 2 * per - 1) / (2 * per), 0, 0, 0, 0, 0, 0, ydt == QL_OUT_BF16 && N % 8 == 0, K, 1};
   // Positions per tile: room for a group of four times the average length, so that few groups take a second pass
   // over their codes, and no more than that: what accumulators and x rows do not take is more stages.  (4096 tokens of
-  // a 64-expert layer, 512 rows per expert: gate/up 1.26 ms with 128, 0.95 with 256; 256 tokens: 0.276 with 64, 0.239
-  // with 128.)
+  // a 64-expert layer, 512 rows per expert: down projection 0.59 ms with 128, 0.41 with 256; 256 tokens, gate/up, when it
+  // was chosen: 0.276 with 64, 0.239 with 128.)
   auto room = [](int n) { return n <= 64 ? 64 : n <= 128 ? 128 : 256; };
   a.nt_max = room((int)std::min<int64_t>(4LL * (g.M / g.G), NT));
   const int steps = (K / 64 + 1) / 2;
@@ -901,9 +904,8 @@ ql_status benq_grouped_mma_launch(const uint8_t *codes, const uint16_t *lut, con
   // one of the stage's earlier uses are over, so the phase's parity tells the one that it waits for.
   a.sa = std::min(SA_MAX, (512 - 2 * a.slot) / 64);
   a.xr = room(a.nt_max) / 2;
-  const int stage = 2 * a.xr * 128;
-  a.xst = std::min(SX_MAX, (XC_RING - SC_MIN * C_BYTES) / stage);
-  if (a.xr == 64) a.xst = 4;
+  const int stage = 2 * a.xr * 128;          // long tiles leave room for three x stages, shorter ones for more codes too
+  a.xst = a.xr == 32 ? SX_MAX : a.xr == 64 ? 4 : (XC_RING - SC_MIN * C_BYTES) / stage;
   static_assert((XC_RING - SC_MIN * C_BYTES) / (NT * 128) >= XPARTS);
   a.sc = std::min(SC_MAX, (XC_RING - a.xst * stage) / C_BYTES);
   // the most tiles that the counts could make (each group may end inside a tile)

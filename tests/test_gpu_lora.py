@@ -190,3 +190,36 @@ def test_lora_add_captured_and_replayed(ql):
         go()
         torch.cuda.synchronize()
         assert all(torch.equal(a, y) for a, (_, _, y) in zip(got, layers))
+
+
+def test_lora_add_on_two_streams_at_once_beside_experts(ql):
+    """Many rows per adapter (both stages' large forms) on two streams, an expert product between the calls of each: the
+    same bits as one call after the other."""
+    T, G, r, K, N = 600, 3, 48, 320, 544
+    gen = torch.Generator(device="cuda").manual_seed(4)
+
+    def rnd(*s):
+        return torch.randn(*s, device="cuda", generator=gen)
+    A, B, x = rnd(G, r, K).bfloat16(), rnd(G, N, r).bfloat16(), rnd(T, K).bfloat16()
+    ws = [synth.benq_weights(N, K, seed=70 + g) for g in range(G)]
+    codes, lut = dev(np.stack([w.codes for w in ws])), bits16(np.stack([w.lut for w in ws]))
+    order, offsets = _plan(ql, torch.randint(-1, G, (T,), generator=gen, **I32).cpu().numpy(), G)
+    rooms = [_room(ql, 1, T, r) for _ in range(2)]
+    outs = [[torch.zeros(T, N, device="cuda") for _ in range(4)] for _ in range(2)]
+
+    def go(i):
+        for y in outs[i]:
+            y.zero_()
+            ql.benq_grouped_linear(codes, lut, x, offsets, y, x_rows=order, y_rows=order)
+            ql.lora_add([(A, B, y)], x, order, offsets, workspace=rooms[i])
+    go(0)
+    torch.cuda.synchronize()
+    want = outs[0][0].clone()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i, s in enumerate(streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            go(i)
+    torch.cuda.synchronize()
+    ql.ql_check()
+    assert all(torch.equal(y, want) for ys in outs for y in ys)

@@ -28,7 +28,8 @@ __device__ __forceinline__ void split(float v, uint16_t (&part)[P]) {
   }
 }
 
-// The tile'th tile of `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
+// The tile'th tile of up to `tt` positions of one group, found by one warp: g (-1: there are fewer tiles) and its positions.
+// A group's tiles are of equal length, so that CTAs with equal numbers of tiles end together.
 // Returns the number of tiles before the group that it stopped at (with tile past the last: the number of all tiles).
 __device__ __forceinline__ int find_tile(const int32_t *offsets, int G, int T, int tt, int tile, int &g, int &p0, int &p1) {
   const int lane = threadIdx.x & 31;
@@ -51,10 +52,12 @@ __device__ __forceinline__ int find_tile(const int32_t *offsets, int G, int T, i
     const unsigned who = __ballot_sync(0xffffffffu, mine);
     if (who) {
       const int src = __ffs(who) - 1;
-      const int at = a + (tile - (carry + s - n)) * tt;
+      const int first = __shfl_sync(0xffffffffu, a, src), end = __shfl_sync(0xffffffffu, b, src);
+      const int before = carry + __shfl_sync(0xffffffffu, s - n, src), of = __shfl_sync(0xffffffffu, n, src);
+      const int per = (end - first + of - 1) / of;
       g = g0 + src;
-      p0 = __shfl_sync(0xffffffffu, at, src);
-      p1 = min(__shfl_sync(0xffffffffu, b, src), p0 + tt);
+      p0 = min(end, first + (tile - before) * per);
+      p1 = min(end, p0 + per);
       return carry;
     }
     carry += __shfl_sync(0xffffffffu, s, 31);

@@ -43,8 +43,7 @@
 #include <type_traits>
 
 #include "ql_internal.cuh"
-#include "pair_gemm.cuh"
-#include "sm100_ptx.cuh"
+#include "grouped_ptx.cuh"
 
 namespace {
 

@@ -20,8 +20,7 @@
 #include <algorithm>
 
 #include "lora.cuh"
-#include "pair_gemm.cuh"
-#include "sm100_ptx.cuh"
+#include "grouped_ptx.cuh"
 
 namespace {
 

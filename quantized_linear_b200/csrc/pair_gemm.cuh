@@ -42,12 +42,6 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
   asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
-// After a wait that ran out: time for this thread block's own copies to land (a few us) before its memory is given up.
-__device__ __forceinline__ void settle() {
-  const long long t0 = clock64();
-  while (clock64() - t0 < (1 << 17)) __nanosleep(1000);
-}
-
 // Bounded wait shared by all roles.  Gives up when the budget runs out or when the pair's abort
 // flag is set; a thread that runs out sets the flag in both CTAs so that the others stop at once.
 struct Waiter {
